@@ -12,9 +12,13 @@ import ctypes as C
 import torch
 
 from . import _native as N
+from .layer import (lin_attn_bwd, lin_attn_fwd, lin_attn_step, lin_attn_workspace_bytes, rms_norm, rms_norm_bwd,
+                    rms_norm_quant, w4_matvec, w4_pack, w4_quantize)
 
 __all__ = ["chunk_fwd", "chunk_bwd", "decode_step", "state_init", "device_status", "chunk_fwd_workspace_bytes",
-           "chunk_bwd_workspace_bytes", "MuirError", "KernelTimer", "launch_count", "gate_proj", "GATE_RANKS"]
+           "chunk_bwd_workspace_bytes", "MuirError", "KernelTimer", "launch_count", "gate_proj", "GATE_RANKS",
+           "lin_attn_fwd", "lin_attn_bwd", "lin_attn_step", "lin_attn_workspace_bytes", "rms_norm", "rms_norm_quant",
+           "rms_norm_bwd", "w4_quantize", "w4_pack", "w4_matvec"]
 
 MuirError = N.MuirError
 

@@ -12,7 +12,7 @@ CHECK_LIB_PATH = os.path.join(_PKG, "libmuir_check.so")
 
 (MUIR_OK, MUIR_ERR_INVALID_ARG, MUIR_ERR_UNSUPPORTED, MUIR_ERR_WORKSPACE, MUIR_ERR_CUDA, MUIR_ERR_TIMEOUT,
  MUIR_ERR_BOUNDS) = range(7)
-MUIR_F32, MUIR_BF16 = 0, 1
+MUIR_F32, MUIR_BF16, MUIR_E4M3 = 0, 1, 2
 MUIR_SAVE_FOR_BWD, MUIR_USE_SAVED = 1, 2
 
 ERROR_NAMES = {MUIR_ERR_INVALID_ARG: "invalid argument", MUIR_ERR_UNSUPPORTED: "unsupported",
@@ -40,6 +40,21 @@ class DecodeArgs(C.Structure):
                 ("log_alpha", vp), ("r", vp), ("r_seq_stride", C.c_int64), ("y", vp)]
 
 
+class LinArgs(C.Structure):
+    _fields_ = [("B", C.c_int64), ("T", C.c_int64), ("H", C.c_int32), ("dk", C.c_int32), ("dv", C.c_int32),
+                ("dtype", C.c_int32), ("flags", C.c_int32), ("scale", C.c_float),
+                ("q", vp), ("k", vp), ("v", vp), ("log_decay", vp), ("lengths", vp), ("S0", vp)]
+
+
+class LinGrads(C.Structure):
+    _fields_ = [("dy", vp), ("dS_T", vp), ("dq", vp), ("dk", vp), ("dv", vp), ("dS0", vp)]
+
+
+class LinStepArgs(C.Structure):
+    _fields_ = [("n_seq", C.c_int64), ("H", C.c_int32), ("dk", C.c_int32), ("dv", C.c_int32), ("dtype", C.c_int32),
+                ("scale", C.c_float), ("S", vp), ("q", vp), ("k", vp), ("v", vp), ("log_decay", vp), ("y", vp)]
+
+
 # Every symbol include/muir.h declares, with its ctypes signature.
 SIGNATURES = {
     "muir_chunk_fwd_workspace": (C.c_size_t, [C.POINTER(ChunkArgs)]),
@@ -55,6 +70,19 @@ SIGNATURES = {
     "muir_apply_map": (C.c_int, [vp, vp, vp, vp, C.c_int64, C.c_int32, C.c_int32, C.c_int32, vp]),
     "muir_gate_proj": (C.c_int, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, C.c_int64, C.c_int32, C.c_int32,
                                  C.c_int32, C.c_int32, vp]),
+    "muir_lin_fwd_workspace": (C.c_size_t, [C.POINTER(LinArgs)]),
+    "muir_lin_fwd": (C.c_int, [C.POINTER(LinArgs), vp, vp, vp, C.c_size_t, vp]),
+    "muir_lin_bwd_workspace": (C.c_size_t, [C.POINTER(LinArgs)]),
+    "muir_lin_bwd": (C.c_int, [C.POINTER(LinArgs), C.POINTER(LinGrads), vp, C.c_size_t, vp]),
+    "muir_lin_step": (C.c_int, [C.POINTER(LinStepArgs), vp]),
+    "muir_rms_norm": (C.c_int, [vp, vp, vp, vp, vp, vp, C.c_int64, C.c_int32, C.c_float, C.c_int32, vp]),
+    "muir_rms_norm_quant": (C.c_int, [vp, vp, vp, vp, vp, vp, vp, C.c_int64, C.c_int32, C.c_float, C.c_int32, vp]),
+    "muir_rms_norm_bwd_workspace": (C.c_size_t, [C.c_int64, C.c_int32]),
+    "muir_rms_norm_bwd": (C.c_int, [vp, vp, vp, vp, vp, vp, vp, C.c_int64, C.c_int32, C.c_int32, vp, C.c_size_t, vp]),
+    "muir_w4_bytes": (C.c_size_t, [C.c_int32, C.c_int32, C.c_int32, C.POINTER(C.c_size_t)]),
+    "muir_w4_quantize": (C.c_int, [vp, vp, vp, C.c_int32, C.c_int32, C.c_int32, C.c_int32, vp]),
+    "muir_w4_pack": (C.c_int, [vp, vp, vp, vp, C.c_int32, C.c_int32, C.c_int32, vp]),
+    "muir_w4_matvec": (C.c_int, [vp, vp, vp, vp, vp, C.c_int64, C.c_int32, C.c_int32, C.c_int32, C.c_int32, C.c_int32, vp]),
     "muir_device_status": (C.c_int, [vp]),
     "muir_last_error": (C.c_char_p, []),
     "muir_version": (C.c_int, []),

@@ -1,0 +1,331 @@
+// Linear attention with one decay per head.
+//
+//   S_t = lambda_h S_{t-1} + k_t v_t^T        y_t = scale S_t^T q_t
+//
+// lambda_h = exp(log_decay[h]) is a constant of the head, so everything that
+// depends on it is a power of one number. Over a run of L tokens with state S
+// before it,
+//
+//   y_i = scale (sum_{s <= i} lambda^{i-s} (q_i . k_s) v_s + lambda^{i+1} S^T q_i)
+//   S'  = lambda^L S + sum_s lambda^{L-1-s} k_s v_s^T.
+//
+// One "pass" computes this for operands called a, b, c (forward: q, k, v) into
+// one output, and the three gradients are passes of the same form:
+//
+//   dq_t = scale sum_{s <= t} lambda^{t-s} (dy_t . v_s) k_s + ...   a, b, c = dy, v, k
+//   dk_s = scale sum_{t >= s} lambda^{t-s} (v_s . dy_t) q_t + ...   a, b, c = v, dy, q, in reverse
+//   dv_s = scale sum_{t >= s} lambda^{t-s} (k_s . q_t) dy_t + ...   a, b, c = k, q, dy, in reverse
+//
+// A reverse pass walks the tokens from the last to the first. Its state after a
+// run is the cotangent dS of the forward state entering that run, which already
+// contains that run's first decay; so with i counted from the run's end, the
+// state term is lambda^i (not i + 1) and the update weight lambda^{L-i} (not
+// L-1-i), and the state after the first token is dS0 with no further factor.
+// dq's state is S^T and dk's is dS^T: those passes read stored states transposed.
+//
+// Work is split over sequences, heads and segments of the tokens (three
+// launches: the segments' own states from zero, their running combination, the
+// outputs), because one sequence of 16 heads alone would fill 16 of 148 SMs.
+//
+// This file holds the CUDA-core form, which serves fp32 inputs at fp32 accuracy.
+#pragma once
+
+#include "common.cuh"
+
+namespace muir {
+
+struct LinPass {
+  const void *a, *b, *c;  // [B,T,H,da], [B,T,H,da], [B,T,H,dc]
+  void* out;              // [B,T,H,dc]
+  const float* log_decay; // [H]
+  const int* lengths;     // [B] valid tokens of each sequence (clamped to [0,T]), or null: T
+  const float* init;      // state before the first token of the walk, [B,H][da][dc] ([dc][da] if init_t), or null
+  float* fin;             // state after the last one, [B,H][da][dc], or null
+  float* seg;             // [B,H,nseg][...] states per segment (workspace), or null when nseg = 1
+  int64_t T, seglen;
+  int B, H, da, dc, nseg;
+  int reverse, init_t, seg_t;
+  float p_scale, o_scale, u_scale;  // of the token-token sum, of the state term, of the state update
+};
+
+// log2(lambda), held above -2^14 so that 0 * log2(lambda) is 0 for lambda = 0
+// (2^-16384 is 0 in fp32 either way). NaN stays NaN.
+__device__ __forceinline__ float lin_log2(const float* log_decay, int h) {
+  const float c = __ldg(log_decay + h) * 1.4426950408889634f;
+  return c < -16384.f ? -16384.f : c;
+}
+
+__device__ __forceinline__ int64_t lin_length(const LinPass& p, int b) {
+  if (!p.lengths) return p.T;
+  const int64_t n = __ldg(p.lengths + b);
+  return n < 0 ? 0 : n > p.T ? p.T : n;
+}
+
+// Valid tokens of segment j of a sequence of len tokens.
+__device__ __forceinline__ int64_t lin_seg_tokens(const LinPass& p, int64_t len, int j) {
+  const int64_t n = len - (int64_t)j * p.seglen;
+  return n < 0 ? 0 : n > p.seglen ? p.seglen : n;
+}
+
+// ---- segment states -> states entering each segment ---------------------------
+//
+// One thread per state element and (b, h): a walk over the segments, in the
+// pass's direction, that replaces each segment's own state by the state that
+// enters it. Every load of the walk is independent, so four are kept in flight.
+__global__ void __launch_bounds__(128) lin_combine_kernel(LinPass p) {
+  const int n = p.da * p.dc;
+  const int bh = blockIdx.y, e = blockIdx.x * 128 + threadIdx.x;
+  if (e >= n) return;
+  const int b = bh / p.H, h = bh % p.H;
+  const float c = lin_log2(p.log_decay, h);
+  const int64_t len = lin_length(p, b);
+  float s = p.init ? __ldg(p.init + (int64_t)bh * n + e) : 0.f;
+  float* q = p.seg + (int64_t)bh * p.nseg * n + e;
+  const int64_t step = p.reverse ? -n : n;
+  if (p.reverse) q += (int64_t)(p.nseg - 1) * n;
+  constexpr int U = 4;
+  for (int j0 = 0; j0 < p.nseg; j0 += U) {
+    float own[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) own[u] = j0 + u < p.nseg ? q[u * step] : 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (j0 + u >= p.nseg) break;
+      q[u * step] = s;
+      const int j = p.reverse ? p.nseg - 1 - (j0 + u) : j0 + u;
+      s = exp2f(c * (float)lin_seg_tokens(p, len, j)) * s + own[u];
+    }
+    q += U * step;
+  }
+  if (p.fin) p.fin[(int64_t)bh * n + e] = s;
+}
+
+// ---- CUDA-core pass -----------------------------------------------------------
+//
+// One CTA of 256 threads per (b, h, segment, 32 columns of c), 32 tokens at a
+// time: the token-token products of the run in shared memory, the state's slab
+// [da][32] in shared memory in fp32. The products are recomputed by each of the
+// dc / 32 slabs, a quarter of the arithmetic at da = dc = 128.
+constexpr int kLinRun = 32;
+
+template <int DA>
+struct LinSmem {
+  float a[kLinRun][DA + 4], b[kLinRun][DA + 4];
+  float c[kLinRun][36], p[kLinRun][36];
+  float s[DA][36];
+  float pw[kLinRun + 2];  // lambda^0 ..
+};
+
+// OUT: write outputs from the entering state; otherwise the segment's own state.
+template <int DA, typename T, bool OUT>
+__global__ void __launch_bounds__(256) lin_simt_kernel(LinPass p) {
+  extern __shared__ __align__(16) uint8_t lin_sm[];
+  LinSmem<DA>& sm = *reinterpret_cast<LinSmem<DA>*>(lin_sm);
+  const int tid = threadIdx.x;
+  const int slabs = p.dc >> 5;
+  int64_t x = blockIdx.x;
+  const int slab = (int)(x % slabs);
+  x /= slabs;
+  const int j = (int)(x % p.nseg);
+  const int bh = (int)(x / p.nseg);
+  const int b = bh / p.H, h = bh % p.H;
+  const int64_t len = lin_length(p, b), t0 = (int64_t)j * p.seglen;
+  const int64_t valid = lin_seg_tokens(p, len, j);
+  const float c2 = lin_log2(p.log_decay, h);
+  const int col0 = slab * 32;
+  const int nstate = DA * p.dc;
+  for (int i = tid; i < kLinRun + 2; i += 256) sm.pw[i] = exp2f(c2 * (float)i);
+
+  // the entering state
+  {
+    const float* src = nullptr;
+    bool tr = false;
+    if constexpr (OUT) {
+      if (p.seg) { src = p.seg + ((int64_t)bh * p.nseg + j) * nstate; tr = p.seg_t; }
+      else if (p.init) { src = p.init + (int64_t)bh * nstate; tr = p.init_t; }
+    }
+    for (int i = tid; i < DA * 32; i += 256) {
+      const int r = i >> 5, cc = i & 31;
+      sm.s[r][cc] = !src ? 0.f : tr ? __ldg(src + (int64_t)(col0 + cc) * DA + r) : __ldg(src + (int64_t)r * p.dc + col0 + cc);
+    }
+  }
+  if constexpr (OUT) {  // padded tokens: zeros
+    const int64_t end = t0 + p.seglen < p.T ? t0 + p.seglen : p.T;
+    for (int64_t i = (t0 + valid) * 8 + tid; i < end * 8; i += 256) {
+      const float z[4] = {0.f, 0.f, 0.f, 0.f};
+      Elt<T>::st4(static_cast<T*>(p.out) + (((int64_t)b * p.T + (i >> 3)) * p.H + h) * p.dc + col0 + (int)(i & 7) * 4, z);
+    }
+  }
+
+  const int64_t runs = (valid + kLinRun - 1) / kLinRun;
+  for (int64_t n = 0; n < runs; ++n) {
+    const int64_t r0 = (p.reverse ? runs - 1 - n : n) * kLinRun;  // first token of the run, in the segment
+    const int L = (int)(valid - r0 < kLinRun ? valid - r0 : kLinRun);
+    const int64_t row = (int64_t)b * p.T + t0 + r0;
+    __syncthreads();
+    for (int i = tid; i < kLinRun * (DA / 4); i += 256) {
+      const int t = i / (DA / 4), c4 = (i % (DA / 4)) * 4;
+      float va[4] = {0.f, 0.f, 0.f, 0.f}, vb[4] = {0.f, 0.f, 0.f, 0.f};
+      if (t < L) {
+        const int64_t o = ((row + t) * p.H + h) * DA + c4;
+        if constexpr (OUT) Elt<T>::ld4(static_cast<const T*>(p.a) + o, va);
+        Elt<T>::ld4(static_cast<const T*>(p.b) + o, vb);
+      }
+      if constexpr (OUT) *reinterpret_cast<float4*>(&sm.a[t][c4]) = make_float4(va[0], va[1], va[2], va[3]);
+      *reinterpret_cast<float4*>(&sm.b[t][c4]) = make_float4(vb[0], vb[1], vb[2], vb[3]);
+    }
+    for (int i = tid; i < kLinRun * 8; i += 256) {
+      const int t = i >> 3, c4 = (i & 7) * 4;
+      float vc[4] = {0.f, 0.f, 0.f, 0.f};
+      if (t < L) Elt<T>::ld4(static_cast<const T*>(p.c) + ((row + t) * p.H + h) * p.dc + col0 + c4, vc);
+      *reinterpret_cast<float4*>(&sm.c[t][c4]) = make_float4(vc[0], vc[1], vc[2], vc[3]);
+    }
+    __syncthreads();
+    const int tr = tid >> 3, cg = (tid & 7) * 4;  // token row, first of 4 columns
+    if constexpr (OUT) {
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int k = 0; k < DA; k += 4) {
+        const float4 av = *reinterpret_cast<const float4*>(&sm.a[tr][k]);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const float4 bv = *reinterpret_cast<const float4*>(&sm.b[(tid & 7) + 8 * m][k]);
+          acc[m] = fmaf(av.x, bv.x, fmaf(av.y, bv.y, fmaf(av.z, bv.z, fmaf(av.w, bv.w, acc[m]))));
+        }
+      }
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const int s = (tid & 7) + 8 * m;
+        const int gap = p.reverse ? s - tr : tr - s;
+        // a masked pair is dropped, not multiplied by zero (rows past L hold zeros)
+        sm.p[tr][s] = gap >= 0 && s < L ? acc[m] * sm.pw[gap] * p.p_scale : 0.f;
+      }
+      __syncthreads();
+      float o[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int s = 0; s < kLinRun; ++s) {
+        const float pv = sm.p[tr][s];
+        const float4 cv = *reinterpret_cast<const float4*>(&sm.c[s][cg]);
+        o[0] = fmaf(pv, cv.x, o[0]); o[1] = fmaf(pv, cv.y, o[1]); o[2] = fmaf(pv, cv.z, o[2]); o[3] = fmaf(pv, cv.w, o[3]);
+      }
+      for (int k = 0; k < DA; ++k) {
+        const float av = sm.a[tr][k];
+        const float4 sv = *reinterpret_cast<const float4*>(&sm.s[k][cg]);
+        u[0] = fmaf(av, sv.x, u[0]); u[1] = fmaf(av, sv.y, u[1]); u[2] = fmaf(av, sv.z, u[2]); u[3] = fmaf(av, sv.w, u[3]);
+      }
+      if (tr < L) {
+        const float w = p.o_scale * sm.pw[p.reverse ? L - 1 - tr : tr + 1];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) o[m] = fmaf(w, u[m], o[m]);
+        Elt<T>::st4(static_cast<T*>(p.out) + ((row + tr) * p.H + h) * p.dc + col0 + cg, o);
+      }
+      __syncthreads();
+    }
+    // S = lambda^L S + sum_s weight_s b_s c_s^T; rows tr, tr + 32, ..
+    float up[DA / 32][4];
+#pragma unroll
+    for (int m = 0; m < DA / 32; ++m)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) up[m][q] = 0.f;
+    for (int s = 0; s < L; ++s) {
+      const float w = p.u_scale * sm.pw[p.reverse ? s + 1 : L - 1 - s];
+      const float4 cv = *reinterpret_cast<const float4*>(&sm.c[s][cg]);
+#pragma unroll
+      for (int m = 0; m < DA / 32; ++m) {
+        const float bw = sm.b[s][tr + 32 * m] * w;
+        up[m][0] = fmaf(bw, cv.x, up[m][0]); up[m][1] = fmaf(bw, cv.y, up[m][1]);
+        up[m][2] = fmaf(bw, cv.z, up[m][2]); up[m][3] = fmaf(bw, cv.w, up[m][3]);
+      }
+    }
+    const float wl = sm.pw[L];
+#pragma unroll
+    for (int m = 0; m < DA / 32; ++m) {
+      float4* d = reinterpret_cast<float4*>(&sm.s[tr + 32 * m][cg]);
+      const float4 v = *d;
+      *d = make_float4(fmaf(wl, v.x, up[m][0]), fmaf(wl, v.y, up[m][1]), fmaf(wl, v.z, up[m][2]), fmaf(wl, v.w, up[m][3]));
+    }
+  }
+  __syncthreads();
+  float* dst = nullptr;
+  if constexpr (!OUT) dst = p.seg + ((int64_t)bh * p.nseg + j) * nstate;
+  else if (p.fin && p.nseg == 1) dst = p.fin + (int64_t)bh * nstate;
+  if (dst)
+    for (int i = tid; i < DA * 32; i += 256) dst[(int64_t)(i >> 5) * p.dc + col0 + (i & 31)] = sm.s[i >> 5][i & 31];
+}
+
+// ---- one token ------------------------------------------------------------------
+//
+// y_j = scale (lambda sum_i q_i S_ij + (q . k) v_j), S_ij <- lambda S_ij + k_i v_j.
+// Memory bound: one CTA per (sequence, head, 32 columns) reads its slab of the
+// state once into registers and writes it once, as the gated-delta-rule step does.
+struct LinStepParams {
+  float* S;
+  const void *q, *k, *v;
+  const float* log_decay;
+  void* y;
+  int H, dv;
+  float scale;
+};
+
+template <int DK, typename T>
+__global__ void __launch_bounds__(128) lin_step_kernel(LinStepParams p) {
+  constexpr int RM = DK / 16;
+  const int tid = threadIdx.x, cg = tid & 7, rg = tid >> 3;
+  const int slabs = p.dv >> 5;
+  const int slab = (int)(blockIdx.x % slabs);
+  const int64_t nh = blockIdx.x / slabs;
+  __shared__ float s_k[DK], s_q[DK], s_red[4][32], s_dot[4];
+
+  float* Sb = p.S + nh * DK * (int64_t)p.dv + slab * 32 + cg * 4;
+  float4 x[RM];
+#pragma unroll
+  for (int m = 0; m < RM; ++m) x[m] = *reinterpret_cast<const float4*>(Sb + (int64_t)(rg + 16 * m) * p.dv);
+  float vj[4];
+  const int64_t co = nh * p.dv + slab * 32 + cg * 4;
+  Elt<T>::ld4(static_cast<const T*>(p.v) + co, vj);
+  float kq = 0.f;
+  if (tid < DK) {
+    const float kk = Elt<T>::ld(static_cast<const T*>(p.k) + nh * DK + tid);
+    const float qq = Elt<T>::ld(static_cast<const T*>(p.q) + nh * DK + tid);
+    s_k[tid] = kk;
+    s_q[tid] = qq;
+    kq = kk * qq;
+  }
+  const float lam = expf(__ldg(p.log_decay + (int)(nh % p.H)));
+  kq = warp_sum(kq);
+  if ((tid & 31) == 0) s_dot[tid >> 5] = kq;
+  __syncthreads();
+  float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int m = 0; m < RM; ++m) {
+    const int i = rg + 16 * m;
+    const float kk = s_k[i], qq = s_q[i];
+    x[m].x *= lam; x[m].y *= lam; x[m].z *= lam; x[m].w *= lam;
+    o[0] = fmaf(qq, x[m].x, o[0]); o[1] = fmaf(qq, x[m].y, o[1]);
+    o[2] = fmaf(qq, x[m].z, o[2]); o[3] = fmaf(qq, x[m].w, o[3]);
+    x[m].x = fmaf(kk, vj[0], x[m].x); x[m].y = fmaf(kk, vj[1], x[m].y);
+    x[m].z = fmaf(kk, vj[2], x[m].z); x[m].w = fmaf(kk, vj[3], x[m].w);
+    *reinterpret_cast<float4*>(Sb + (int64_t)i * p.dv) = x[m];
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    o[c] += __shfl_xor_sync(0xffffffffu, o[c], 8);
+    o[c] += __shfl_xor_sync(0xffffffffu, o[c], 16);
+  }
+  const int warp = tid >> 5, lane = tid & 31;
+  if (lane < 8) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) s_red[warp][lane * 4 + c] = o[c];
+  }
+  __syncthreads();
+  if (tid < 8) {
+    const float KQ = s_dot[0] + s_dot[1] + s_dot[2] + s_dot[3];
+    float yo[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int jj = cg * 4 + c;
+      yo[c] = p.scale * fmaf(KQ, vj[c], s_red[0][jj] + s_red[1][jj] + s_red[2][jj] + s_red[3][jj]);
+    }
+    Elt<T>::st4(static_cast<T*>(p.y) + co, yo);
+  }
+}
+
+}  // namespace muir

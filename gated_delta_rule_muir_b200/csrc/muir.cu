@@ -18,6 +18,7 @@
 #include "chunk_bwd.cuh"
 #include "gate_proj.cuh"
 #include "gate_proj_tma.cuh"
+#include "host.h"
 
 namespace {
 
@@ -90,6 +91,29 @@ bool dim_ok(int d) { return d == 32 || d == 64 || d == 128; }
 
 }  // namespace
 
+// What the library's other translation units use of this one (host.h).
+namespace muir_host {
+void clear_error() { g_err.clear(); }
+int fail(int code, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  return ::fail(code, "%s", buf);
+}
+int check_launch(const char* what) { return cuda_check(what); }
+void* launch_begin(const char* name, cudaStream_t s) {
+  Launch l(name, s);
+  cudaEvent_t b = l.b;
+  l.b = nullptr;  // recorded by launch_end instead
+  return b;
+}
+void launch_end(void* event, cudaStream_t s) {
+  if (event) cudaEventRecord(static_cast<cudaEvent_t>(event), s);
+}
+}  // namespace muir_host
+
 extern "C" {
 
 int muir_version(void) { return 103; }
@@ -103,6 +127,9 @@ int muir_device_status(void* stream) {
   unsigned int host = 0, zero = 0;
   if (cudaMemcpyFromSymbol(&host, muir::g_status, sizeof host) != cudaSuccess) return cuda_check("read status");
   if (cudaMemcpyToSymbol(muir::g_status, &zero, sizeof zero) != cudaSuccess) return cuda_check("clear status");
+  unsigned int layer = 0;  // the word of the layer operators' translation unit
+  if (!muir_host::take_layer_status(&layer)) return cuda_check("read status");
+  host |= layer;
   if (host & muir::kStatusTimeout) return fail(MUIR_ERR_TIMEOUT, "a bounded device wait expired");
   if (host & muir::kStatusBounds)
     return fail(MUIR_ERR_BOUNDS, "an index failed its bounds check (checking build):%s%s%s",

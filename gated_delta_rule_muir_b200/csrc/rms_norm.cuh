@@ -1,0 +1,236 @@
+// Root-mean-square norm of token rows, with the residual's addition.
+//
+//   h = x + residual                         (h = x without a residual)
+//   rstd = (mean_d h_d^2 + eps)^(-1/2)
+//   y_d = h_d rstd weight_d
+//
+// y in the input's type, or in 8 bits: with top = max_d |y_d|, scale = top / 448
+// (448 is e4m3's largest number) and q_d = e4m3(y_d 448 / top), so that
+// q_d scale ~ y_d; a row of zeros has scale 0 and codes 0. The norm is taken of
+// the fp32 sum; the residual stream h that is written out is rounded once, to the
+// input's type. Statistics are fp32.
+//
+// Backward, with xh = h rstd and g = dy weight:
+//   dx_d = rstd (g_d - xh_d mean_d(g xh)) + dh_d      dweight_d = sum_rows dy_d xh_d
+// dx is the gradient of x and of the residual alike; dh is the cotangent of the
+// written residual stream.
+//
+// Memory bound: every row is read once, kept in registers across its reduction
+// and written once. Rows up to 1024 wide take a warp each (eight rows per CTA, no
+// barrier); wider rows take one CTA.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace muir {
+
+struct NormParams {
+  const void *x, *residual;
+  const float* weight;
+  void *y, *h;
+  uint8_t* q;
+  float *scale, *rstd;
+  int64_t n;
+  int d;
+  float eps;
+};
+
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float warp_max_nan(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+// The reductions of one row over its NT threads: a warp, or a CTA of NT threads
+// (slot: shared array of 32 floats per call, so that one barrier is enough).
+template <int NT>
+__device__ __forceinline__ float row_sum(float x, float* slot) {
+  x = warp_sum(x);
+  if constexpr (NT > 32) {
+    if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = warp_sum((threadIdx.x & 31) < NT / 32 ? slot[threadIdx.x & 31] : 0.f);
+  }
+  return x;
+}
+template <int NT>
+__device__ __forceinline__ float row_max(float x, float* slot) {
+  x = warp_max_nan(x);
+  if constexpr (NT > 32) {
+    if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = warp_max_nan((threadIdx.x & 31) < NT / 32 ? slot[threadIdx.x & 31] : 0.f);
+  }
+  return x;
+}
+
+// NT threads per row, V pieces of 8 elements per thread: piece (v, thread) holds
+// elements 8 (v NT + thread) .. + 7, absent past d.
+template <typename T, int NT, int V, bool QUANT>
+__global__ void __launch_bounds__(NT > 32 ? NT : 256) rms_norm_kernel(NormParams p) {
+  __shared__ float slot[2][32];
+  constexpr int ROWS = NT > 32 ? 1 : 8;
+  const int lane = NT > 32 ? threadIdx.x : threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * ROWS + (NT > 32 ? 0 : threadIdx.x >> 5);
+  if (row >= p.n) return;  // whole warps (NT = 32) or no one
+  const int64_t off = row * p.d;
+  float x[V][8];
+  float ss = 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = (v * NT + lane) * 8;
+    if (e < p.d) {
+      Elt<T>::ld8(static_cast<const T*>(p.x) + off + e, x[v]);
+      if (p.residual) {
+        float r[8];
+        Elt<T>::ld8(static_cast<const T*>(p.residual) + off + e, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[v][i] += r[i];
+        Elt<T>::st8(static_cast<T*>(p.h) + off + e, x[v]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[v][i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = fmaf(x[v][i], x[v][i], ss);
+  }
+  ss = row_sum<NT>(ss, slot[0]);
+  const float rstd = 1.f / sqrtf(ss / (float)p.d + p.eps);
+  if (lane == 0 && p.rstd) p.rstd[row] = rstd;
+  float top = 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = (v * NT + lane) * 8;
+    if (e < p.d) {
+      float w[8];
+      Elt<float>::ld8(p.weight + e, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[v][i] = x[v][i] * rstd * w[i];
+        top = max_nan(top, fabsf(x[v][i]));
+      }
+      if constexpr (!QUANT) Elt<T>::st8(static_cast<T*>(p.y) + off + e, x[v]);
+    }
+  }
+  if constexpr (QUANT) {
+    top = row_max<NT>(top, slot[1]);
+    if (lane == 0) p.scale[row] = top / 448.f;
+    // 448 / top overflows below 1.4e-36: such a row is brought up by 2^100 first
+    const float up = top < 1e-30f ? 0x1p100f : 1.f;
+    const float inv = top == 0.f ? 0.f : 448.f / (top * up);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = (v * NT + lane) * 8;
+      if (e < p.d) {
+        uint32_t w[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          float s[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[i] = x[v][4 * k + i] * up * inv;
+          const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(s[0], s[1]), __NV_SATFINITE, __NV_E4M3);
+          const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(s[2], s[3]), __NV_SATFINITE, __NV_E4M3);
+          w[k] = lo | (hi << 16);
+        }
+        *reinterpret_cast<uint2*>(p.q + off + e) = make_uint2(w[0], w[1]);
+      }
+    }
+  }
+}
+
+struct NormBwdParams {
+  const void *dy, *h, *dh;
+  const float *weight, *rstd;
+  void* dx;
+  float *dweight, *part;  // part: [gridDim.x][d]
+  int64_t n;
+  int d;
+};
+
+// Each CTA walks rows blockIdx.x, + gridDim.x, .. and keeps its threads' share of
+// dweight in registers; the partial sums go to the workspace and are added in a
+// fixed order by rms_norm_dw_kernel, so that a repeated call gives the same bits.
+template <typename T, int NT, int V>
+__global__ void __launch_bounds__(NT) rms_norm_bwd_kernel(NormBwdParams p) {
+  __shared__ float slot[2][32];
+  const int lane = threadIdx.x;
+  float dw[V][8], w[V][8];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = (v * NT + lane) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) { dw[v][i] = 0.f; w[v][i] = 0.f; }
+    if (e < p.d) Elt<float>::ld8(p.weight + e, w[v]);
+  }
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < p.n; row += gridDim.x, turn ^= 1) {
+    const int64_t off = row * p.d;
+    const float rstd = __ldg(p.rstd + row);
+    float xh[V][8], g[V][8];
+    float dot = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = (v * NT + lane) * 8;
+      if (e < p.d) {
+        Elt<T>::ld8(static_cast<const T*>(p.h) + off + e, xh[v]);
+        Elt<T>::ld8(static_cast<const T*>(p.dy) + off + e, g[v]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          xh[v][i] *= rstd;
+          dw[v][i] = fmaf(g[v][i], xh[v][i], dw[v][i]);
+          g[v][i] *= w[v][i];
+          dot = fmaf(g[v][i], xh[v][i], dot);
+        }
+      }
+    }
+    dot = row_sum<NT>(dot, slot[turn]) / (float)p.d;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = (v * NT + lane) * 8;
+      if (e < p.d) {
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = rstd * fmaf(-xh[v][i], dot, g[v][i]);
+        if (p.dh) {
+          float r[8];
+          Elt<T>::ld8(static_cast<const T*>(p.dh) + off + e, r);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] += r[i];
+        }
+        Elt<T>::st8(static_cast<T*>(p.dx) + off + e, o);
+      }
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = (v * NT + lane) * 8;
+    if (e < p.d) Elt<float>::st8(p.part + (int64_t)blockIdx.x * p.d + e, dw[v]);
+  }
+}
+
+// dweight = the column sums of part [m][d]: 32 columns per CTA, 32 x 8 threads.
+__global__ void __launch_bounds__(256) rms_norm_dw_kernel(const float* __restrict__ part, float* __restrict__ dweight, int m,
+                                                          int d) {
+  __shared__ float s[8][33];
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5;
+  float a = 0.f;
+  if (c < d)
+    for (int i = r; i < m; i += 8) a += part[(int64_t)i * d + c];
+  s[r][threadIdx.x & 31] = a;
+  __syncthreads();
+  if (r == 0 && c < d) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) a += s[i][threadIdx.x];
+    dweight[c] = a;
+  }
+}
+
+}  // namespace muir

@@ -1,0 +1,296 @@
+"""The operators around the state update: linear attention with one decay per head,
+RMS norm with the residual's addition, products with 4-bit weights.
+
+As in the rest of the binding, each function only checks shapes, dtypes and
+devices, allocates outputs and workspace with torch, and calls the C ABI
+(include/muir.h). Work goes to `stream` (default: the current stream of the
+operands' device); what a call allocates is allocated for that stream.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes as C
+
+import torch
+
+from . import _native as N
+
+_E4M3 = torch.float8_e4m3fn
+
+
+def _ptr(t):
+    return None if t is None else C.c_void_p(t.data_ptr())
+
+
+def _need(t, name, shape, dtype, device):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}")
+    if t.shape != torch.Size(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: must be a contiguous CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the other operands on {device}")
+
+
+def _dims(t, name, n):
+    if t.dim() != n:
+        raise ValueError(f"{name}: expected {n} dimensions, got shape {tuple(t.shape)}")
+    return t.shape
+
+
+def _io_code(t, name):
+    code = {torch.float32: N.MUIR_F32, torch.bfloat16: N.MUIR_BF16}.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: expected float32 or bfloat16, got {t.dtype}")
+    return code
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """The operands' device and the launch stream made current, for allocations and launches."""
+    if device.type != "cuda":
+        raise ValueError(f"operands must be CUDA tensors, got {device}")
+    with torch.cuda.device(device):
+        s = torch.cuda.current_stream() if stream is None else stream
+        if s.device != device:
+            raise ValueError(f"stream of {s.device}, operands on {device}")
+        with torch.cuda.stream(s):
+            yield C.c_void_p(s.cuda_stream)
+
+
+def _workspace(nbytes, device, ws):
+    if ws is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    if not ws.is_cuda or ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
+    if ws.numel() * ws.element_size() < nbytes:
+        raise ValueError("workspace too small")
+    return ws
+
+
+def _out(t, name, shape, dtype, device):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(t, name, shape, dtype, device)
+    return t
+
+
+def _lin_args(q, k, v, log_decay, scale, lengths, S0):
+    B, T, H, dk = _dims(q, "q", 4)
+    dv = _dims(v, "v", 4)[3]
+    dev = q.device
+    code = _io_code(q, "q")
+    _need(q, "q", (B, T, H, dk), q.dtype, dev)
+    _need(k, "k", (B, T, H, dk), q.dtype, dev)
+    _need(v, "v", (B, T, H, dv), q.dtype, dev)
+    _need(log_decay, "log_decay", (H,), torch.float32, dev)
+    if lengths is not None:
+        _need(lengths, "lengths", (B,), torch.int32, dev)
+    if S0 is not None:
+        _need(S0, "S0", (B, H, dk, dv), torch.float32, dev)
+    a = N.LinArgs(B=B, T=T, H=H, dk=dk, dv=dv, dtype=code, flags=0, scale=float(scale), q=_ptr(q), k=_ptr(k), v=_ptr(v),
+                  log_decay=_ptr(log_decay), lengths=_ptr(lengths), S0=_ptr(S0))
+    return a, (B, T, H, dk, dv, q.dtype, dev)
+
+
+def lin_attn_workspace_bytes(q, k, v, log_decay, *, backward=False) -> int:
+    """Bytes of workspace that lin_attn_fwd (or lin_attn_bwd) needs for operands of these sizes."""
+    a, _ = _lin_args(q, k, v, log_decay, 1.0, None, None)
+    lib = N.load()
+    return int((lib.muir_lin_bwd_workspace if backward else lib.muir_lin_fwd_workspace)(C.byref(a)))
+
+
+def lin_attn_fwd(q, k, v, log_decay, *, scale=1.0, lengths=None, S0=None, want_state=True, y=None, S_T=None,
+                 workspace=None, stream=None):
+    """Linear attention with one decay per head, S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T,
+    y_t = scale S_t^T q_t, over whole sequences: q, k [B,T,H,dk], v [B,T,H,dv] (fp32 or bf16),
+    log_decay [H] fp32 (<= 0), lengths [B] int32 (valid tokens of a padded batch), S0
+    [B,H,dk,dv] fp32. Returns (y [B,T,H,dv], S_T [B,H,dk,dv] fp32 or None); y is zero at padded
+    tokens and S_T is the state after the last valid one. The decays are constants: they get
+    no gradient."""
+    a, (B, T, H, dk, dv, dt, dev) = _lin_args(q, k, v, log_decay, scale, lengths, S0)
+    lib = N.load()
+    with _on(dev, stream) as s:
+        y = _out(y, "y", (B, T, H, dv), dt, dev)
+        S_T = _out(S_T, "S_T", (B, H, dk, dv), torch.float32, dev) if want_state else None
+        nbytes = int(lib.muir_lin_fwd_workspace(C.byref(a)))
+        ws = _workspace(nbytes, dev, workspace)
+        N.check(lib.muir_lin_fwd(C.byref(a), _ptr(y), _ptr(S_T), _ptr(ws), nbytes, s), "muir_lin_fwd")
+    return y, S_T
+
+
+def lin_attn_bwd(q, k, v, log_decay, dy, *, scale=1.0, lengths=None, S0=None, dS_T=None, want_dS0=True, outputs=None,
+                 workspace=None, stream=None):
+    """Gradients of lin_attn_fwd: a dict of dq, dk, dv (shaped and typed like q, k, v) and dS0
+    [B,H,dk,dv] fp32 (None if not wanted). `outputs` (a dict from an earlier call) is reused."""
+    a, (B, T, H, dk, dv, dt, dev) = _lin_args(q, k, v, log_decay, scale, lengths, S0)
+    _need(dy, "dy", (B, T, H, dv), dt, dev)
+    if dS_T is not None:
+        _need(dS_T, "dS_T", (B, H, dk, dv), torch.float32, dev)
+    lib = N.load()
+    o = outputs or {}
+    with _on(dev, stream) as s:
+        out = {"dq": _out(o.get("dq"), "dq", (B, T, H, dk), dt, dev), "dk": _out(o.get("dk"), "dk", (B, T, H, dk), dt, dev),
+               "dv": _out(o.get("dv"), "dv", (B, T, H, dv), dt, dev),
+               "dS0": _out(o.get("dS0"), "dS0", (B, H, dk, dv), torch.float32, dev) if want_dS0 else None}
+        g = N.LinGrads(dy=_ptr(dy), dS_T=_ptr(dS_T), **{n: _ptr(t) for n, t in out.items()})
+        nbytes = int(lib.muir_lin_bwd_workspace(C.byref(a)))
+        ws = _workspace(nbytes, dev, workspace)
+        N.check(lib.muir_lin_bwd(C.byref(a), C.byref(g), _ptr(ws), nbytes, s), "muir_lin_bwd")
+    return out
+
+
+def lin_attn_step(S, q, k, v, log_decay, *, scale=1.0, y=None, stream=None):
+    """One token of lin_attn_fwd for n sequences: S [n,H,dk,dv] fp32 updated in place, q, k
+    [n,H,dk], v [n,H,dv]. Returns y [n,H,dv]."""
+    n, H, dk, dv = _dims(S, "S", 4)
+    dev = S.device
+    code = _io_code(q, "q")
+    _need(S, "S", (n, H, dk, dv), torch.float32, dev)
+    for name, t, d in (("q", q, dk), ("k", k, dk), ("v", v, dv)):
+        _need(t, name, (n, H, d), q.dtype, dev)
+    _need(log_decay, "log_decay", (H,), torch.float32, dev)
+    lib = N.load()
+    with _on(dev, stream) as s:
+        y = _out(y, "y", (n, H, dv), q.dtype, dev)
+        a = N.LinStepArgs(n_seq=n, H=H, dk=dk, dv=dv, dtype=code, scale=float(scale), S=_ptr(S), q=_ptr(q), k=_ptr(k),
+                          v=_ptr(v), log_decay=_ptr(log_decay), y=_ptr(y))
+        N.check(lib.muir_lin_step(C.byref(a), s), "muir_lin_step")
+    return y
+
+
+def _norm_operands(x, weight, residual):
+    n, d = _dims(x, "x", 2)
+    dev = x.device
+    code = _io_code(x, "x")
+    _need(x, "x", (n, d), x.dtype, dev)
+    _need(weight, "weight", (d,), torch.float32, dev)
+    if residual is not None:
+        _need(residual, "residual", (n, d), x.dtype, dev)
+    return n, d, dev, code
+
+
+def rms_norm(x, weight, *, residual=None, eps=1e-6, y=None, h=None, rstd=None, stream=None):
+    """RMS norm of rows x [n,d] (fp32 or bf16), weight [d] fp32, with the residual's addition:
+    h = x + residual, y = h (mean h^2 + eps)^(-1/2) weight. Returns a dict of y, rstd [n] fp32
+    and, with a residual, h (the new residual stream; may be the residual's own buffer)."""
+    n, d, dev, code = _norm_operands(x, weight, residual)
+    lib = N.load()
+    with _on(dev, stream) as s:
+        out = {"y": _out(y, "y", (n, d), x.dtype, dev), "rstd": _out(rstd, "rstd", (n,), torch.float32, dev)}
+        if residual is not None:
+            out["h"] = _out(h, "h", (n, d), x.dtype, dev)
+        N.check(lib.muir_rms_norm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(out["y"]), _ptr(out.get("h")), _ptr(out["rstd"]),
+                                  n, d, float(eps), code, s), "muir_rms_norm")
+    return out
+
+
+def rms_norm_quant(x, weight, *, residual=None, eps=1e-6, q=None, scale=None, h=None, rstd=None, stream=None):
+    """rms_norm with its output in 8 bits: q [n,d] float8_e4m3fn and scale [n] fp32, q scale ~ y,
+    scale = max |y| / 448 of the row. Returns a dict of q, scale, rstd and, with a residual, h."""
+    n, d, dev, code = _norm_operands(x, weight, residual)
+    lib = N.load()
+    with _on(dev, stream) as s:
+        out = {"q": _out(q, "q", (n, d), _E4M3, dev), "scale": _out(scale, "scale", (n,), torch.float32, dev),
+               "rstd": _out(rstd, "rstd", (n,), torch.float32, dev)}
+        if residual is not None:
+            out["h"] = _out(h, "h", (n, d), x.dtype, dev)
+        N.check(lib.muir_rms_norm_quant(_ptr(x), _ptr(residual), _ptr(weight), _ptr(out["q"]), _ptr(out["scale"]),
+                                        _ptr(out.get("h")), _ptr(out["rstd"]), n, d, float(eps), code, s),
+                "muir_rms_norm_quant")
+    return out
+
+
+def rms_norm_bwd(dy, h, weight, rstd, *, dh=None, dx=None, dweight=None, workspace=None, stream=None):
+    """Gradients of rms_norm from its h (its x, without a residual) and rstd: (dx [n,d], dweight
+    [d] fp32). dx is the gradient of x and of the residual alike; dh is the cotangent of h."""
+    n, d = _dims(h, "h", 2)
+    dev = h.device
+    code = _io_code(h, "h")
+    _need(h, "h", (n, d), h.dtype, dev)
+    _need(dy, "dy", (n, d), h.dtype, dev)
+    _need(weight, "weight", (d,), torch.float32, dev)
+    _need(rstd, "rstd", (n,), torch.float32, dev)
+    if dh is not None:
+        _need(dh, "dh", (n, d), h.dtype, dev)
+    lib = N.load()
+    with _on(dev, stream) as s:
+        dx = _out(dx, "dx", (n, d), h.dtype, dev)
+        dweight = _out(dweight, "dweight", (d,), torch.float32, dev)
+        nbytes = int(lib.muir_rms_norm_bwd_workspace(n, d))
+        ws = _workspace(nbytes, dev, workspace)
+        N.check(lib.muir_rms_norm_bwd(_ptr(dy), _ptr(h), _ptr(weight), _ptr(rstd), _ptr(dh), _ptr(dx), _ptr(dweight), n, d,
+                                      code, _ptr(ws), nbytes, s), "muir_rms_norm_bwd")
+    return dx, dweight
+
+
+def w4_quantize(w, *, group=128, stream=None):
+    """Weights [O,K] (fp32 or bf16) to 4 bits: (codes [O,K] uint8 in 0..15, scales [O,K/group]
+    bf16), w ~ scale (code - 8), scale = max |w| / 7 of each group."""
+    O, K = _dims(w, "w", 2)
+    dev = w.device
+    code = _io_code(w, "w")
+    _need(w, "w", (O, K), w.dtype, dev)
+    if group not in (32, 64, 128) or K % 128:
+        raise ValueError(f"group must be 32, 64 or 128 and K a multiple of 128 (got {group}, {K})")
+    lib = N.load()
+    with _on(dev, stream) as s:
+        codes = torch.empty(O, K, dtype=torch.uint8, device=dev)
+        scales = torch.empty(O, K // group, dtype=torch.bfloat16, device=dev)
+        N.check(lib.muir_w4_quantize(_ptr(w), _ptr(codes), _ptr(scales), K, O, group, code, s), "muir_w4_quantize")
+    return codes, scales
+
+
+def w4_pack(codes, scales, *, stream=None):
+    """Codes [O,K] uint8 and scales [O,K/group] bf16 in the layout of w4_matvec: (wq uint8
+    [ceil(O/16), K/128, 1024], ws bf16 [ceil(O/16), K/128, 128/group, 16]); see include/muir.h."""
+    O, K = _dims(codes, "codes", 2)
+    ng = _dims(scales, "scales", 2)[1]
+    dev = codes.device
+    if K % 128 or ng == 0 or K % ng or K // ng not in (32, 64, 128):
+        raise ValueError(f"K must be a multiple of 128 in groups of 32, 64 or 128 (got K={K}, {ng} groups)")
+    group = K // ng
+    _need(codes, "codes", (O, K), torch.uint8, dev)
+    _need(scales, "scales", (O, ng), torch.bfloat16, dev)
+    lib = N.load()
+    tiles = (O + 15) // 16
+    with _on(dev, stream) as s:
+        wq = torch.empty(tiles, K // 128, 1024, dtype=torch.uint8, device=dev)
+        ws = torch.empty(tiles, K // 128, 128 // group, 16, dtype=torch.bfloat16, device=dev)
+        N.check(lib.muir_w4_pack(_ptr(codes), _ptr(scales), _ptr(wq), _ptr(ws), K, O, group, s), "muir_w4_pack")
+    return wq, ws
+
+
+def w4_matvec(x, wq, ws, O, *, x_scale=None, out_dtype=None, y=None, stream=None):
+    """y [n,O] = x [n,K] times the transposed 4-bit weights (wq, ws of w4_pack, O outputs). x:
+    fp32 or bf16 (y of the same type), or float8_e4m3fn with x_scale [n] fp32, as rms_norm_quant
+    gives them (y bf16, or fp32 by out_dtype). Meant for few rows: weights are read once per 32."""
+    n, K = _dims(x, "x", 2)
+    dev = x.device
+    tiles, blocks, _ = _dims(wq, "wq", 3)
+    gpb = _dims(ws, "ws", 4)[2]
+    if gpb not in (1, 2, 4):
+        raise ValueError(f"ws: expected 1, 2 or 4 groups per block of 128 inputs, got {gpb}")
+    if K != blocks * 128 or not 0 < O <= tiles * 16 or O <= (tiles - 1) * 16:
+        raise ValueError(f"wq holds {blocks * 128} inputs and {tiles} tiles of 16 outputs; got K={K}, O={O}")
+    eight = x.dtype == _E4M3
+    code = N.MUIR_E4M3 if eight else _io_code(x, "x")
+    ydt = (out_dtype or torch.bfloat16) if eight else x.dtype
+    if out_dtype not in (None, ydt) or ydt not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"out_dtype {out_dtype} with x of {x.dtype}")
+    _need(x, "x", (n, K), x.dtype, dev)
+    _need(wq, "wq", (tiles, blocks, 1024), torch.uint8, dev)
+    _need(ws, "ws", (tiles, blocks, gpb, 16), torch.bfloat16, dev)
+    if x_scale is not None:
+        if not eight:
+            raise ValueError("x_scale belongs to 8-bit rows")
+        _need(x_scale, "x_scale", (n,), torch.float32, dev)
+    lib = N.load()
+    with _on(dev, stream) as s:
+        y = _out(y, "y", (n, O), ydt, dev)
+        N.check(lib.muir_w4_matvec(_ptr(x), _ptr(x_scale), _ptr(wq), _ptr(ws), _ptr(y), n, K, O, 128 // gpb, code,
+                                   N.MUIR_F32 if ydt == torch.float32 else N.MUIR_BF16, s), "muir_w4_matvec")
+    return y

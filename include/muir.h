@@ -59,6 +59,7 @@ extern "C" {
 
 #define MUIR_F32 0
 #define MUIR_BF16 1
+#define MUIR_E4M3 2 /* 8-bit rows: rms_norm_quant's output, w4_matvec's input */
 
 /* Bits of muir_chunk_args.flags (every other bit must be 0). */
 #define MUIR_SAVE_FOR_BWD 1 /* muir_chunk_fwd: also leave in the workspace what muir_chunk_bwd needs */
@@ -279,6 +280,123 @@ int muir_row_scale(const float* S, int64_t n_seq, int32_t H, int32_t dk, int32_t
 int muir_gate_proj(const void* x, const void* w_down, const void* u_decay, const void* u_erase, const void* u_out,
                    const void* u_write, const void* u_read, float* log_alpha, void* e, void* z, void* w, void* g,
                    int64_t n_tokens, int32_t d_model, int32_t ok, int32_t ov, int32_t dtype, void* stream);
+
+/* ---- Around the state update --------------------------------------------------
+ *
+ * Linear attention with one decay per head: the state update without the
+ * channel-wise decay, the erase and the gates,
+ *
+ *   S_t = lambda_h S_{t-1} + k_t v_t^T        y_t = scale S_t^T q_t
+ *
+ * with lambda_h = exp(log_decay[h]) a constant of the head, log_decay <= 0 (-inf
+ * is allowed: no memory). Sums, states and decay powers are fp32; the decays get no
+ * gradient. Layouts and dtypes as for muir_chunk_fwd; dk, dv in {32, 64, 128}; any
+ * T >= 0 (no padding to a chunk is needed), B H <= 65535, T <= 2^30.
+ *
+ * lengths, where not NULL, gives the valid tokens of each sequence of a padded
+ * batch (clamped to [0, T]); tokens behind them are not read, whatever they
+ * hold, S_T is the state after the last valid token, and y and the gradients of
+ * padded tokens are written as zeros. */
+typedef struct muir_lin_args {
+  int64_t B;      /* sequences */
+  int64_t T;      /* tokens per sequence */
+  int32_t H;      /* heads */
+  int32_t dk, dv; /* rows and columns of the state */
+  int32_t dtype;  /* MUIR_F32 or MUIR_BF16: q, k, v, y and their gradients */
+  int32_t flags;  /* 0 */
+  float scale;
+  const void* q;          /* [B,T,H,dk] */
+  const void* k;          /* [B,T,H,dk] */
+  const void* v;          /* [B,T,H,dv] */
+  const float* log_decay; /* [H] */
+  const int32_t* lengths; /* [B], or NULL: every sequence has T tokens */
+  const float* S0;        /* [B,H,dk,dv] initial state, or NULL for zeros */
+} muir_lin_args;
+
+/* Forward over a whole sequence. y [B,T,H,dv] (dtype); S_T [B,H,dk,dv], or NULL
+ * if not wanted (S_T = S0 in place is allowed). ws: at least
+ * muir_lin_fwd_workspace(a) bytes, 256-byte aligned (0 bytes: may be NULL); the
+ * query reads sizes and dtype only and returns 0 when they are invalid. */
+size_t muir_lin_fwd_workspace(const muir_lin_args* a);
+int muir_lin_fwd(const muir_lin_args* a, void* y, float* S_T, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradients of muir_lin_fwd, written (not accumulated). */
+typedef struct muir_lin_grads {
+  const void* dy;    /* [B,T,H,dv] cotangent of y (dtype) */
+  const float* dS_T; /* [B,H,dk,dv] cotangent of S_T, or NULL for zeros */
+  void* dq;          /* [B,T,H,dk] (dtype) */
+  void* dk;          /* [B,T,H,dk] (dtype) */
+  void* dv;          /* [B,T,H,dv] (dtype) */
+  float* dS0;        /* [B,H,dk,dv], or NULL */
+} muir_lin_grads;
+
+/* Backward pass with the forward's arguments; the states are recomputed. ws: at
+ * least muir_lin_bwd_workspace(a) bytes, 256-byte aligned. */
+size_t muir_lin_bwd_workspace(const muir_lin_args* a);
+int muir_lin_bwd(const muir_lin_args* a, const muir_lin_grads* g, void* ws, size_t ws_bytes, void* stream);
+
+/* One token for n_seq sequences; the state is read and written once, in place. */
+typedef struct muir_lin_step_args {
+  int64_t n_seq;
+  int32_t H, dk, dv;
+  int32_t dtype;  /* of q, k, v, y */
+  float scale;
+  float* S;       /* [n_seq,H,dk,dv] */
+  const void* q;  /* [n_seq,H,dk] */
+  const void* k;  /* [n_seq,H,dk] */
+  const void* v;  /* [n_seq,H,dv] */
+  const float* log_decay; /* [H] */
+  void* y;        /* [n_seq,H,dv] */
+} muir_lin_step_args;
+int muir_lin_step(const muir_lin_step_args* a, void* stream);
+
+/* RMS norm of token rows [n,d] with the residual's addition, as a layer applies it
+ * ahead of its projections:
+ *     h = x + residual (x alone where residual is NULL)
+ *     rstd = (mean_d h^2 + eps)^(-1/2)        y = h rstd weight
+ * x, residual, y and h have the given dtype, weight [d] is float; statistics are
+ * fp32 and the norm is taken of the unrounded sum. h is required with a residual
+ * and ignored without one; it may be the residual's buffer or x's, and y may be x's.
+ * rstd [n] may be NULL. d: a multiple of 8 up to 16384; n >= 0.
+ * muir_rms_norm_quant writes the norm in 8 bits (e4m3) instead, with a scale per
+ * row: scale = max_d |y| / 448 and q the nearest e4m3 number to y / scale, so that
+ * q scale ~ y; a row of zeros has scale 0 and q 0. */
+int muir_rms_norm(const void* x, const void* residual, const float* weight, void* y, void* h, float* rstd, int64_t n,
+                  int32_t d, float eps, int32_t dtype, void* stream);
+int muir_rms_norm_quant(const void* x, const void* residual, const float* weight, void* q, float* scale, void* h,
+                        float* rstd, int64_t n, int32_t d, float eps, int32_t dtype, void* stream);
+
+/* Backward of muir_rms_norm from the forward's h (x without a residual) and rstd:
+ * dx [n,d] is the gradient of x and of the residual alike, dweight [d] is float.
+ * dh, the cotangent of the written h, may be NULL. dx may be dy's, dh's or h's
+ * buffer. Sums over the rows are added in a fixed order. */
+size_t muir_rms_norm_bwd_workspace(int64_t n, int32_t d);
+int muir_rms_norm_bwd(const void* dy, const void* h, const float* weight, const float* rstd, const void* dh, void* dx,
+                      float* dweight, int64_t n, int32_t d, int32_t dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* Product of a few rows with 4-bit weights and group scales, the projections of a
+ * decode step:
+ *     y[n][o] = x_scale[n] sum_k x[n][k] scale[o][k / group] (code[o][k] - 8)
+ * K a multiple of 128, group 32, 64 or 128, any O > 0 and n >= 0 (weights are read
+ * once per 32 rows). x [n][K]: MUIR_F32 or MUIR_BF16 with y of the same type, or
+ * MUIR_E4M3 with y of either type and x_scale [n] (NULL: 1). Sums are fp32.
+ *
+ * The weights are laid out once: muir_w4_quantize makes codes [O][K] (one byte
+ * each, 0..15) and bf16 scales [O][K/group] from weights [O][K] (MUIR_F32 or
+ * MUIR_BF16, finite; scale = max |w| / 7 of a group), and muir_w4_pack lays codes
+ * and scales out for the product: muir_w4_bytes gives the bytes of the packed
+ * codes and of the packed scales. Layout: tiles of 16 outputs x 128 inputs of 1024
+ * bytes, [ceil(O/16)][K/128]; in a tile, 32 bytes for each (g, t), g = 0..7,
+ * t = 0..3: for the outputs g and g + 8 four 4-byte words j = 0..3, word j with the
+ * inputs 32 j + 8 t .. + 7, lowest nibble first. Scales
+ * [ceil(O/16)][K/128][128/group][16]. Outputs past O have code 8 and scale 0. */
+size_t muir_w4_bytes(int32_t K, int32_t O, int32_t group, size_t* scale_bytes);
+int muir_w4_quantize(const void* w, void* codes, void* scales, int32_t K, int32_t O, int32_t group, int32_t dtype,
+                     void* stream);
+int muir_w4_pack(const void* codes, const void* scales, void* wq, void* ws, int32_t K, int32_t O, int32_t group,
+                 void* stream);
+int muir_w4_matvec(const void* x, const float* x_scale, const void* wq, const void* ws, void* y, int64_t n, int32_t K,
+                   int32_t O, int32_t group, int32_t x_dtype, int32_t y_dtype, void* stream);
 
 /* Synchronises `stream`, then returns and clears the device-side status word:
  * MUIR_OK, or MUIR_ERR_TIMEOUT if a kernel's bounded wait expired since the

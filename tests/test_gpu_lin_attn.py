@@ -1,0 +1,234 @@
+"""Linear attention with one decay per head against the fp64 recurrence.
+
+Tolerances, elementwise. A is the same sum over absolute values (layer_oracle's _abs).
+A chain of n fp32 additions and products errs by at most n 2^-24 A; the longest chain
+is a dot of 128 channels, the tokens' sum and the carried state, n <= 128 + T + 64.
+With bf16 operands the tensor cores take the token-token weights and the state each
+rounded once to bf16 (2^-8 relative, so 2^-8 A in all), and a bf16 output is rounded
+once more (2^-8 |y|). States and dS0 are fp32 sums of exact products in both types."""
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_muir_b200 as muir
+from oracle import layer_oracle as lo
+
+pytestmark = pytest.mark.gpu
+
+
+def _tol(dtype, ref, A, T, out):
+    n = (192 + T) * 2.0 ** -24 * A + 1e-30
+    return n if dtype == torch.float32 or not out else n + 2.0 ** -8 * (np.abs(ref) + (1 + 2.0 ** -7) * A) + 1e-30
+
+
+def _check(name, got, ref, A, T, dtype, out=True):
+    got = got.detach().double().cpu().numpy()
+    assert np.isfinite(got).all(), name
+    over = np.abs(got - ref) - _tol(dtype, ref, A, T, out)
+    assert over.max(initial=-1.0) <= 0, f"{name}: over the bound by {over.max():.3g} at {np.unravel_index(over.argmax(), over.shape)}"
+
+
+def _make(B, T, H, dk, dv, dtype, seed=0, log_decay=None):
+    r = np.random.default_rng(seed)
+    unit = lambda x: x / np.sqrt((x * x).sum(-1, keepdims=True))
+    d = {"q": unit(r.normal(size=(B, T, H, dk))), "k": unit(r.normal(size=(B, T, H, dk))), "v": r.normal(size=(B, T, H, dv)),
+         "dy": r.normal(size=(B, T, H, dv)), "S0": r.normal(size=(B, H, dk, dv)), "dS_T": r.normal(size=(B, H, dk, dv))}
+    t = {}
+    for n, x in d.items():
+        t[n] = torch.tensor(x, dtype=torch.float32).to(torch.float32 if n in ("S0", "dS_T") else dtype).cuda()
+        d[n] = t[n].double().cpu().numpy()
+    ld = -np.exp(r.uniform(np.log(1e-4), np.log(0.7), H)) if log_decay is None else np.array(log_decay)
+    t["ld"] = torch.tensor(ld, dtype=torch.float32).cuda()
+    d["ld"] = t["ld"].double().cpu().numpy()
+    return d, t
+
+
+def _run(d, t, dtype, lengths, scale, state):
+    T = d["q"].shape[1]
+    L = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    S0, dS = ("S0", "dS_T") if state else (None, None)
+    y, S = muir.lin_attn_fwd(t["q"], t["k"], t["v"], t["ld"], scale=scale, lengths=L, S0=t.get(S0))
+    g = muir.lin_attn_bwd(t["q"], t["k"], t["v"], t["ld"], t["dy"], scale=scale, lengths=L, S0=t.get(S0), dS_T=t.get(dS))
+    a = (d["q"], d["k"], d["v"], d["ld"])
+    yr, Sr = lo.lin_forward(*a, scale, lengths, d.get(S0))
+    yA, SA = lo.lin_forward_abs(*a, scale, lengths, d.get(S0))
+    _check("y", y, yr, yA, T, t["q"].dtype)
+    _check("S_T", S, Sr, SA, T, t["q"].dtype, out=False)
+    gr = lo.lin_backward(*a, d["dy"], scale, lengths, d.get(S0), d.get(dS))
+    gA = lo.lin_backward_abs(*a, d["dy"], scale, lengths, d.get(S0), d.get(dS))
+    for n in ("dq", "dk", "dv"):
+        _check(n, g[n], gr[n], gA[n], T, t["q"].dtype)
+    _check("dS0", g["dS0"], gr["dS0"], gA["dS0"], T, t["q"].dtype, out=False)
+    assert muir.device_status() == 0
+    return y, S, g
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("case", [
+    (1, 1, 1, 32, 32), (2, 1, 3, 128, 128), (1, 31, 2, 64, 32), (1, 33, 1, 128, 64), (3, 127, 2, 32, 128),
+    (1, 128, 2, 128, 128), (1, 129, 2, 64, 64), (2, 255, 1, 128, 32), (1, 300, 2, 128, 128), (1, 515, 1, 64, 128),
+    (1, 1025, 1, 32, 64), (1, 640, 2, 128, 128)])
+def test_forward_and_gradients(cuda_ok, dtype, case):
+    d, t = _make(*case, dtype)
+    _run(d, t, dtype, None, 0.125, True)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("lengths", [[0, 0, 0], [300, 1, 0], [128, 129, 255], [700, -3, 300], [256, 7, 299]])
+def test_padded_batches_do_not_read_padding(cuda_ok, dtype, lengths):
+    d, t = _make(3, 300, 2, 64, 128, dtype, seed=1)
+    for b, n in enumerate(lengths):
+        n = min(300, max(0, n))
+        for x in ("q", "k", "v", "dy"):
+            t[x][b, n:] = float("nan")
+            t[x][b, n::2] = float("inf")
+            d[x][b, n:] = 0.0
+    y, _, g = _run(d, t, dtype, lengths, 1.0, True)
+    for b, n in enumerate(lengths):
+        n = min(300, max(0, n))
+        for x in (y, g["dq"], g["dk"], g["dv"]):
+            assert (x[b, n:] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("state", [False, True])
+def test_extreme_decays_and_scales(cuda_ok, dtype, state):
+    ld = [0.0, -1e-4, -0.05, -3.0, -80.0, -1e30, -float("inf")]
+    d, t = _make(1, 290, len(ld), 32, 32, dtype, seed=2, log_decay=ld)
+    for scale in (1.0, -0.5, 0.0):
+        with np.errstate(invalid="ignore"):
+            _run(d, t, dtype, None, scale, state)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_no_tokens(cuda_ok, dtype):
+    d, t = _make(2, 0, 2, 32, 64, dtype)
+    y, S = muir.lin_attn_fwd(t["q"], t["k"], t["v"], t["ld"], S0=t["S0"])
+    assert y.shape == (2, 0, 2, 64) and torch.equal(S, t["S0"])
+    g = muir.lin_attn_bwd(t["q"], t["k"], t["v"], t["ld"], t["dy"], S0=t["S0"], dS_T=t["dS_T"])
+    assert torch.equal(g["dS0"], t["dS_T"])
+    y, S = muir.lin_attn_fwd(t["q"], t["k"], t["v"], t["ld"])
+    assert (S == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_differences(cuda_ok, dtype):
+    """The loss is linear in each of q, k, v and S0, so a difference of any length is exact
+    but for rounding: sum |dy| tol(y) + sum |dS_T| tol(S_T), plus the gradient's own."""
+    T = 200
+    d, t = _make(1, T, 2, 64, 64, dtype, seed=3)
+    g = muir.lin_attn_bwd(t["q"], t["k"], t["v"], t["ld"], t["dy"], S0=t["S0"], dS_T=t["dS_T"])
+    r = torch.Generator().manual_seed(4)
+
+    def loss(x):
+        y, S = muir.lin_attn_fwd(x["q"], x["k"], x["v"], t["ld"], S0=x["S0"])
+        dn = {n: v.double().cpu().numpy() for n, v in x.items()}
+        yA, SA = lo.lin_forward_abs(dn["q"], dn["k"], dn["v"], d["ld"], 1.0, None, dn["S0"])
+        slack = (np.abs(d["dy"]) * _tol(dtype, yA, yA, T, True)).sum() + (np.abs(d["dS_T"]) * _tol(dtype, SA, SA, T, False)).sum()
+        return (y.double() * t["dy"].double()).sum().item() + (S.double() * t["dS_T"].double()).sum().item(), slack
+    base = {n: t[n] for n in ("q", "k", "v", "S0")}
+    gA = lo.lin_backward_abs(d["q"], d["k"], d["v"], d["ld"], d["dy"], 1.0, None, d["S0"], d["dS_T"])
+    for n, gn in (("q", "dq"), ("k", "dk"), ("v", "dv"), ("S0", "dS0")):
+        # 256 times the operand: the difference stands far above the slack
+        step = (256.0 * torch.randn(t[n].shape, generator=r)).to(t[n].dtype).cuda()
+        moved = dict(base, **{n: (t[n].float() + step.float()).to(t[n].dtype)})
+        real = moved[n].double() - t[n].double()
+        (l1, s1), (l0, s0) = loss(moved), loss(base)
+        want = (g[gn].double() * real).sum().item()
+        own = (np.abs(real.cpu().numpy()) * _tol(dtype, gA[gn], gA[gn], T, n != "S0")).sum()
+        assert abs(l1 - l0 - want) <= s1 + s0 + own, n
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_steps_continue_a_prompt(cuda_ok, dtype):
+    B, T, n, H = 2, 140, 5, 3
+    d, t = _make(B, T + n, H, 64, 128, dtype, seed=5)
+    y, S = muir.lin_attn_fwd(t["q"][:, :T].contiguous(), t["k"][:, :T].contiguous(), t["v"][:, :T].contiguous(), t["ld"], scale=0.3)
+    a = (d["q"], d["k"], d["v"], d["ld"])
+    yr, Sr = lo.lin_forward(*a, 0.3)
+    yA, SA = lo.lin_forward_abs(*a, 0.3)
+    for i in range(T, T + n):
+        o = muir.lin_attn_step(S, *[t[x][:, i].contiguous() for x in "qkv"], t["ld"], scale=0.3)
+        _check("y", o, yr[:, i], yA[:, i], T + n, dtype)
+    _check("S", S, Sr, SA, T + n, dtype, out=False)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("dims", [(32, 32), (32, 128), (64, 64), (128, 32), (128, 128)])
+def test_step(cuda_ok, dtype, dims):
+    d, t = _make(5, 1, 4, *dims, dtype, seed=6, log_decay=[0.0, -0.3, -20.0, -float("inf")])
+    S = t["S0"].clone()
+    y = muir.lin_attn_step(S, *[t[x][:, 0].contiguous() for x in "qkv"], t["ld"], scale=2.0)
+    yr, Sr = lo.lin_forward(d["q"], d["k"], d["v"], d["ld"], 2.0, None, d["S0"])
+    yA, SA = lo.lin_forward_abs(d["q"], d["k"], d["v"], d["ld"], 2.0, None, d["S0"])
+    _check("y", y, yr[:, 0], yA[:, 0], 1, dtype)
+    _check("S", S, Sr, SA, 1, dtype, out=False)
+    assert muir.lin_attn_step(S[:0], *[t[x][:0, 0].contiguous() for x in "qkv"], t["ld"]).shape == (0, 4, dims[1])
+
+
+def test_state_in_place(cuda_ok):
+    d, t = _make(2, 700, 2, 64, 64, torch.bfloat16, seed=7)
+    y, S = muir.lin_attn_fwd(t["q"], t["k"], t["v"], t["ld"], S0=t["S0"])
+    S2 = t["S0"].clone()
+    y2, _ = muir.lin_attn_fwd(t["q"], t["k"], t["v"], t["ld"], S0=S2, S_T=S2)
+    assert torch.equal(S, S2) and torch.equal(y, y2)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_repeats_streams_and_graphs_agree(cuda_ok, dtype):
+    d, t = _make(2, 1100, 2, 128, 64, dtype, seed=8)
+    L = torch.tensor([1100, 901], dtype=torch.int32, device="cuda")
+
+    def both(stream=None, **kw):
+        y, S = muir.lin_attn_fwd(t["q"], t["k"], t["v"], t["ld"], lengths=L, S0=t["S0"], stream=stream)
+        g = muir.lin_attn_bwd(t["q"], t["k"], t["v"], t["ld"], t["dy"], lengths=L, S0=t["S0"], dS_T=t["dS_T"], stream=stream)
+        return [y, S, *g.values()]
+    want = both()
+    assert all(torch.equal(a, b) for a, b in zip(both(), want))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = both(side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graphs = []
+    for _ in range(2):  # two graphs, replayed in turn
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            out = both()
+        graphs.append((gr, out))
+    for gr, _ in graphs * 2:
+        gr.replay()
+    torch.cuda.synchronize()
+    for _, out in graphs:
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_offsets_past_32_bits(cuda_ok):
+    """2.2e9 elements per operand: the last tokens against the recurrence over the ones that
+    still weigh (exp(-0.25 * 400) is below fp32's least number)."""
+    T, H, D, n = 1_060_000, 16, 128, 400
+    g = torch.Generator(device="cuda").manual_seed(0)
+    q, k, v = (torch.randn(1, T, H, D, generator=g, device="cuda", dtype=torch.bfloat16) for _ in range(3))
+    ld = torch.full((H,), -0.25, device="cuda")
+    y, S = muir.lin_attn_fwd(q, k, v, ld, scale=0.01)
+    a = [x[:, -n:, -2:].double().cpu().numpy() for x in (q, k, v)]
+    ldn = np.full(2, -0.25)
+    yr, Sr = lo.lin_forward(*a, ldn, 0.01)
+    yA, SA = lo.lin_forward_abs(*a, ldn, 0.01)
+    _check("y", y[:, -8:, -2:], yr[:, -8:], yA[:, -8:], n, torch.bfloat16)
+    _check("S_T", S[:, -2:], Sr, SA, n, torch.bfloat16, out=False)
+
+
+def test_refusals_on_the_device(cuda_ok):
+    _, t = _make(1, 8, 2, 32, 32, torch.float32)
+    with pytest.raises(ValueError, match="contiguous"):
+        muir.lin_attn_fwd(t["q"].transpose(1, 2).contiguous().transpose(1, 2), t["k"], t["v"], t["ld"])
+    with pytest.raises(TypeError, match="k"):
+        muir.lin_attn_fwd(t["q"], t["k"].bfloat16(), t["v"], t["ld"])
+    with pytest.raises(TypeError, match="lengths"):
+        muir.lin_attn_fwd(t["q"], t["k"], t["v"], t["ld"], lengths=torch.tensor([8], device="cuda"))
+    with pytest.raises(muir.MuirError, match="unsupported"):
+        muir.lin_attn_fwd(*[torch.zeros(1, 8, 2, 48, device="cuda") for _ in range(3)], t["ld"])
+    with pytest.raises(ValueError, match="workspace too small"):
+        x = torch.zeros(1, 4096, 1, 32, device="cuda")
+        muir.lin_attn_fwd(x, x, x, t["ld"][:1].contiguous(), workspace=torch.empty(16, device="cuda"))
