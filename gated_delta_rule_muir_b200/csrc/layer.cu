@@ -4,6 +4,7 @@
 #include "../../include/muir.h"
 #include "host.h"
 #include "lin_attn.cuh"
+#include "lin_attn_tc.cuh"
 #include "rms_norm.cuh"
 #include "w4.cuh"
 
@@ -46,20 +47,54 @@ int check_ptrs(const char* who, const Ptr (&ptrs)[N]) {
 // ---- linear attention -----------------------------------------------------------
 
 struct LinPlan {
+  bool tc;  // the tensor-core pass
   int nseg;
   int64_t seglen;
 };
 
-// Segments of the CUDA-core pass: two CTAs of work for each SM (two fit at d = 128),
-// at least 8 runs per segment so that its start (a state in and out) stays small.
-LinPlan lin_plan(const muir_lin_args* a, int dc) {
-  const int64_t runs = a->T > 0 ? (a->T + muir::kLinRun - 1) / muir::kLinRun : 1;
-  const int64_t units = a->B * a->H * (dc / 32);
-  int64_t n = (2 * kSMs + units - 1) / units;
-  if (n > runs / 8) n = runs / 8;
-  if (n < 1) n = 1;
+// bf16 operands go to the tensor cores, fp32 ones to the CUDA cores (one bf16
+// rounding of the weights would be all of fp32's accuracy). A box of the copies
+// covers 64 channels, so a token row has at least that many.
+bool lin_use_tc(const muir_lin_args* a) {
+  return a->dtype == MUIR_BF16 && a->T > 0 && (int64_t)a->H * a->dk >= 64 && (int64_t)a->H * a->dv >= 64;
+}
+
+// Segments of the sequence: `passes` passes of output per (sequence, head) share a launch.
+//
+// Tensor cores, one CTA per SM: the split with the least cost, in chunk times, of
+// the waves of CTAs (each with a start and an end worth about 3 chunks), the
+// segments' own states where there is more than one (which read two of three
+// operands again: half as much again) and the walk over them.
+//
+// CUDA cores: two CTAs for each SM, at least 8 runs per segment so that its start
+// (a state in and out) stays small.
+LinPlan lin_plan(const muir_lin_args* a, int passes) {
+  LinPlan pl{lin_use_tc(a), 1, 0};
+  const int64_t run = pl.tc ? muir::kLtChunk : muir::kLinRun;
+  const int64_t runs = a->T > 0 ? (a->T + run - 1) / run : 1;
+  int64_t n = 1;
+  if (pl.tc) {
+    const int64_t units = a->B * a->H * passes;
+    double best = 0.0;
+    for (int64_t c = 1; c <= runs && c <= 1024; ++c) {
+      const double waves = (double)((units * c + kSMs - 1) / kSMs);
+      const double cost = waves * ((double)((runs + c - 1) / c) * (c > 1 ? 1.5 : 1.0) + 3.0) + (c > 1 ? 4.0 + 0.1 * (double)c : 0.0);
+      if (c == 1 || cost < best) {
+        best = cost;
+        n = c;
+      }
+    }
+  } else {
+    const int dmin = a->dk < a->dv && passes > 1 ? a->dk : a->dv;
+    const int64_t units = a->B * a->H * (dmin / 32);
+    n = (2 * kSMs + units - 1) / units;
+    if (n > runs / 8) n = runs / 8;
+    if (n < 1) n = 1;
+  }
   const int64_t per = (runs + n - 1) / n;
-  return LinPlan{(int)((runs + per - 1) / per), per * muir::kLinRun};
+  pl.nseg = (int)((runs + per - 1) / per);
+  pl.seglen = per * run;
+  return pl;
 }
 
 int lin_validate(const muir_lin_args* a, const char* who) {
@@ -108,16 +143,54 @@ int lin_simt_da(const muir::LinPass& p, const char* name, cudaStream_t s) {
   return p.da == 32 ? lin_simt<32, T, OUT>(p, name, s) : p.da == 64 ? lin_simt<64, T, OUT>(p, name, s)
                                                                      : lin_simt<128, T, OUT>(p, name, s);
 }
-// The states entering the segments (p.b, p.c, p.seg), and the final one.
-int lin_states(const muir::LinPass& p, int dtype, const char* name, cudaStream_t s) {
-  int rc = dtype == MUIR_BF16 ? lin_simt_da<bf16, false>(p, name, s) : lin_simt_da<float, false>(p, name, s);
-  if (rc) return rc;
-  LaunchScope l("lin_combine", s);
-  muir::lin_combine_kernel<<<dim3((unsigned)(p.da * p.dc / 128), (unsigned)(p.B * p.H)), 128, 0, s>>>(p);
-  return check_launch("lin_combine");
+int lin_simt_pass(const muir::LinPass& p, int dtype, bool out, const char* name, cudaStream_t s) {
+  if (dtype == MUIR_BF16) return out ? lin_simt_da<bf16, true>(p, name, s) : lin_simt_da<bf16, false>(p, name, s);
+  return out ? lin_simt_da<float, true>(p, name, s) : lin_simt_da<float, false>(p, name, s);
 }
-int lin_outputs(const muir::LinPass& p, int dtype, const char* name, cudaStream_t s) {
-  return dtype == MUIR_BF16 ? lin_simt_da<bf16, true>(p, name, s) : lin_simt_da<float, true>(p, name, s);
+
+template <bool OUT>
+int lin_tc(const muir::LinPass* p, int n, const char* name, cudaStream_t s) {
+  muir::LinTcArgs args{};
+  for (int i = 0; i < n; ++i) {
+    const muir::LinPass& q = p[i];
+    const uint64_t ra = (uint64_t)q.H * q.da, rc = (uint64_t)q.H * q.dc;
+    if ((OUT && !muir_host::make_tmap_bf16_3d(&args.a[i], q.a, ra, (uint64_t)q.T, (uint64_t)q.B, muir::kLtChunk)) ||
+        !muir_host::make_tmap_bf16_3d(&args.b[i], q.b, ra, (uint64_t)q.T, (uint64_t)q.B, muir::kLtChunk) ||
+        !muir_host::make_tmap_bf16_3d(&args.c[i], q.c, rc, (uint64_t)q.T, (uint64_t)q.B, muir::kLtChunk))
+      return fail(MUIR_ERR_CUDA, "%s: tensor map encoding failed", name);
+    args.p[i] = q;
+  }
+  const int64_t blocks = (int64_t)p->B * p->H * p->nseg;
+  if (blocks > kMaxBlocks) return fail(MUIR_ERR_UNSUPPORTED, "%s: too many blocks", name);
+  if (int rc = set_smem(muir::lin_tc_kernel<OUT>, muir::kLtSmem)) return rc;
+  LaunchScope l(name, s);
+  muir::lin_tc_kernel<OUT><<<dim3((unsigned)blocks, (unsigned)n), muir::kLtThreads, muir::kLtSmem, s>>>(args);
+  return check_launch(name);
+}
+
+// `states`: the passes whose segment states are made and combined (none for one
+// segment), `outs`: the passes that write outputs.
+int lin_run(const LinPlan& pl, int dtype, const muir::LinPass* states, int ns, const muir::LinPass* outs, int no,
+            const char* name, cudaStream_t s) {
+  int rc = MUIR_OK;
+  if (pl.nseg > 1) {
+    if (pl.tc) {
+      if ((rc = lin_tc<false>(states, ns, "lin_state", s))) return rc;
+    } else {
+      for (int i = 0; i < ns; ++i)
+        if ((rc = lin_simt_pass(states[i], dtype, false, "lin_state", s))) return rc;
+    }
+    muir::LinCombineArgs ca{};
+    for (int i = 0; i < ns; ++i) ca.p[i] = states[i];
+    const muir::LinPass& p = states[0];
+    LaunchScope l("lin_combine", s);
+    muir::lin_combine_kernel<<<dim3((unsigned)(p.da * p.dc / 128), (unsigned)(p.B * p.H), (unsigned)ns), 128, 0, s>>>(ca);
+    if ((rc = check_launch("lin_combine"))) return rc;
+  }
+  if (pl.tc) return lin_tc<true>(outs, no, name, s);
+  for (int i = 0; i < no; ++i)
+    if ((rc = lin_simt_pass(outs[i], dtype, true, name, s))) return rc;
+  return MUIR_OK;
 }
 
 muir::LinPass lin_pass(const muir_lin_args* x, const LinPlan& pl, int da, int dc) {
@@ -141,7 +214,7 @@ extern "C" {
 size_t muir_lin_fwd_workspace(const muir_lin_args* a) {
   muir_host::clear_error();
   if (lin_validate(a, "lin_fwd") || lin_empty(a)) return 0;
-  return lin_seg_bytes(a, lin_plan(a, a->dv));
+  return lin_seg_bytes(a, lin_plan(a, 1));
 }
 
 int muir_lin_fwd(const muir_lin_args* a, void* y, float* S_T, void* ws, size_t ws_bytes, void* stream) {
@@ -152,7 +225,7 @@ int muir_lin_fwd(const muir_lin_args* a, void* y, float* S_T, void* ws, size_t w
   if ((rc = lin_pointers(a, "lin_fwd"))) return rc;
   const Ptr outs[] = {{y, "y", a->T == 0}, {S_T, "S_T", true}};
   if ((rc = check_ptrs("lin_fwd", outs))) return rc;
-  const LinPlan pl = lin_plan(a, a->dv);
+  const LinPlan pl = lin_plan(a, 1);
   const size_t need = lin_seg_bytes(a, pl);
   if (need && (!ws || !aligned(ws, 256) || ws_bytes < need))
     return fail(MUIR_ERR_WORKSPACE, "lin_fwd: workspace needs %zu bytes, 256-byte aligned", need);
@@ -167,14 +240,13 @@ int muir_lin_fwd(const muir_lin_args* a, void* y, float* S_T, void* ws, size_t w
   p.seg = need ? static_cast<float*>(ws) : nullptr;
   p.p_scale = p.o_scale = a->scale;
   p.u_scale = 1.f;
-  if (p.seg && (rc = lin_states(p, a->dtype, "lin_state", s))) return rc;
-  return lin_outputs(p, a->dtype, "lin_fwd", s);
+  return lin_run(pl, a->dtype, &p, 1, &p, 1, "lin_fwd", s);
 }
 
 size_t muir_lin_bwd_workspace(const muir_lin_args* a) {
   muir_host::clear_error();
   if (lin_validate(a, "lin_bwd") || lin_empty(a)) return 0;
-  const LinPlan pl = lin_plan(a, a->dk < a->dv ? a->dk : a->dv);
+  const LinPlan pl = lin_plan(a, 3);
   return 2 * lin_seg_bytes(a, pl);
 }
 
@@ -189,7 +261,10 @@ int muir_lin_bwd(const muir_lin_args* a, const muir_lin_grads* g, void* ws, size
   const Ptr ptrs[] = {{g->dy, "dy", no_tokens}, {g->dq, "dq", no_tokens}, {g->dk, "dk", no_tokens}, {g->dv, "dv", no_tokens},
                       {g->dS_T, "dS_T", true}, {g->dS0, "dS0", true}};
   if ((rc = check_ptrs("lin_bwd", ptrs))) return rc;
-  const LinPlan pl = lin_plan(a, a->dk < a->dv ? a->dk : a->dv);
+  // the passes run side by side: one may still read these while dS0 is written
+  if (g->dS0 && (g->dS0 == g->dS_T || g->dS0 == a->S0))
+    return fail(MUIR_ERR_INVALID_ARG, "lin_bwd: dS0 must not be dS_T's or S0's buffer");
+  const LinPlan pl = lin_plan(a, 3);
   const size_t seg = lin_seg_bytes(a, pl);
   if (seg && (!ws || !aligned(ws, 256) || ws_bytes < 2 * seg))
     return fail(MUIR_ERR_WORKSPACE, "lin_bwd: workspace needs %zu bytes, 256-byte aligned", 2 * seg);
@@ -197,54 +272,53 @@ int muir_lin_bwd(const muir_lin_args* a, const muir_lin_grads* g, void* ws, size
   float* S = seg ? static_cast<float*>(ws) : nullptr;
   float* dS = seg ? reinterpret_cast<float*>(static_cast<char*>(ws) + seg) : nullptr;
 
+  // the gradients with the longest walk back first; states of dv's and dk's pass, and of dq's
+  muir::LinPass p[3], st[2];
   // dv: keys against queries, cotangents summed, from the last token to the first
-  muir::LinPass p = lin_pass(a, pl, a->dk, a->dv);
-  p.a = a->k;
-  p.b = a->q;
-  p.c = g->dy;
-  p.out = g->dv;
-  p.init = g->dS_T;
-  p.fin = g->dS0;
-  p.seg = dS;
-  p.reverse = 1;
-  p.p_scale = p.u_scale = a->scale;
-  p.o_scale = 1.f;
-  if (dS && (rc = lin_states(p, a->dtype, "lin_dstate", s))) return rc;
-  if ((rc = lin_outputs(p, a->dtype, "lin_dv", s))) return rc;
+  p[0] = lin_pass(a, pl, a->dk, a->dv);
+  p[0].a = a->k;
+  p[0].b = a->q;
+  p[0].c = g->dy;
+  p[0].out = g->dv;
+  p[0].init = g->dS_T;
+  p[0].fin = g->dS0;
+  p[0].seg = dS;
+  p[0].reverse = 1;
+  p[0].p_scale = p[0].u_scale = a->scale;
+  p[0].o_scale = 1.f;
+  st[0] = p[0];
   // dk: values against cotangents, queries summed; the state is dS^T
-  muir::LinPass pk = lin_pass(a, pl, a->dv, a->dk);
-  pk.a = a->v;
-  pk.b = g->dy;
-  pk.c = a->q;
-  pk.out = g->dk;
-  pk.init = g->dS_T;
-  pk.init_t = 1;
-  pk.seg = dS;
-  pk.seg_t = 1;
-  pk.reverse = 1;
-  pk.p_scale = pk.u_scale = a->scale;
-  pk.o_scale = 1.f;
-  if ((rc = lin_outputs(pk, a->dtype, "lin_dk", s))) return rc;
+  p[1] = lin_pass(a, pl, a->dv, a->dk);
+  p[1].a = a->v;
+  p[1].b = g->dy;
+  p[1].c = a->q;
+  p[1].out = g->dk;
+  p[1].init = g->dS_T;
+  p[1].init_t = 1;
+  p[1].seg = dS;
+  p[1].seg_t = 1;
+  p[1].reverse = 1;
+  p[1].p_scale = p[1].u_scale = a->scale;
+  p[1].o_scale = 1.f;
   // dq: cotangents against values, keys summed, forward; the state is S^T
-  muir::LinPass ps = lin_pass(a, pl, a->dk, a->dv);
-  ps.b = a->k;
-  ps.c = a->v;
-  ps.init = a->S0;
-  ps.seg = S;
-  ps.u_scale = 1.f;
-  if (S && (rc = lin_states(ps, a->dtype, "lin_state", s))) return rc;
-  muir::LinPass pq = lin_pass(a, pl, a->dv, a->dk);
-  pq.a = g->dy;
-  pq.b = a->v;
-  pq.c = a->k;
-  pq.out = g->dq;
-  pq.init = a->S0;
-  pq.init_t = 1;
-  pq.seg = S;
-  pq.seg_t = 1;
-  pq.p_scale = pq.o_scale = a->scale;
-  pq.u_scale = 1.f;
-  return lin_outputs(pq, a->dtype, "lin_dq", s);
+  p[2] = lin_pass(a, pl, a->dv, a->dk);
+  p[2].a = g->dy;
+  p[2].b = a->v;
+  p[2].c = a->k;
+  p[2].out = g->dq;
+  p[2].init = a->S0;
+  p[2].init_t = 1;
+  p[2].seg = S;
+  p[2].seg_t = 1;
+  p[2].p_scale = p[2].o_scale = a->scale;
+  p[2].u_scale = 1.f;
+  st[1] = lin_pass(a, pl, a->dk, a->dv);
+  st[1].b = a->k;
+  st[1].c = a->v;
+  st[1].init = a->S0;
+  st[1].seg = S;
+  st[1].u_scale = 1.f;
+  return lin_run(pl, a->dtype, st, 2, p, 3, "lin_bwd", s);
 }
 
 int muir_lin_step(const muir_lin_step_args* a, void* stream) {

@@ -72,7 +72,11 @@ __device__ __forceinline__ int64_t lin_seg_tokens(const LinPass& p, int64_t len,
 // One thread per state element and (b, h): a walk over the segments, in the
 // pass's direction, that replaces each segment's own state by the state that
 // enters it. Every load of the walk is independent, so four are kept in flight.
-__global__ void __launch_bounds__(128) lin_combine_kernel(LinPass p) {
+struct LinCombineArgs {
+  LinPass p[2];
+};
+__global__ void __launch_bounds__(128) lin_combine_kernel(const __grid_constant__ LinCombineArgs args) {
+  const LinPass& p = args.p[blockIdx.z];
   const int n = p.da * p.dc;
   const int bh = blockIdx.y, e = blockIdx.x * 128 + threadIdx.x;
   if (e >= n) return;

@@ -327,7 +327,7 @@ typedef struct muir_lin_grads {
   void* dq;          /* [B,T,H,dk] (dtype) */
   void* dk;          /* [B,T,H,dk] (dtype) */
   void* dv;          /* [B,T,H,dv] (dtype) */
-  float* dS0;        /* [B,H,dk,dv], or NULL */
+  float* dS0;        /* [B,H,dk,dv], or NULL; not dS_T's or S0's buffer */
 } muir_lin_grads;
 
 /* Backward pass with the forward's arguments; the states are recomputed. ws: at
