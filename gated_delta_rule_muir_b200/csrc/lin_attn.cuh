@@ -55,6 +55,19 @@ __device__ __forceinline__ float lin_log2(const float* log_decay, int h) {
   return c < -16384.f ? -16384.f : c;
 }
 
+// lambda^L as the two factors of a state's decay, S lambda^L + x = g S + (e S + x).
+// Near 1 the power is 1 + e with e = lambda^L - 1, good to 24 bits of e: a state that
+// is carried over thousands of steps by a power rounded to 24 bits of itself would
+// be off by thousands of roundings of the same sign.
+struct LinDecay {
+  float g, e;
+  __device__ __forceinline__ float operator()(float S, float x) const { return fmaf(g, S, fmaf(e, S, x)); }
+};
+__device__ __forceinline__ LinDecay lin_decay(float c2, int64_t L) {
+  const float x = c2 * (float)L, w = exp2f(x);
+  return w > 0.5f ? LinDecay{1.f, expm1f(x * 0.6931471805599453f)} : LinDecay{w, 0.f};
+}
+
 __device__ __forceinline__ int64_t lin_length(const LinPass& p, int b) {
   if (!p.lengths) return p.T;
   const int64_t n = __ldg(p.lengths + b);
@@ -97,7 +110,7 @@ __global__ void __launch_bounds__(128) lin_combine_kernel(const __grid_constant_
       if (j0 + u >= p.nseg) break;
       q[u * step] = s;
       const int j = p.reverse ? p.nseg - 1 - (j0 + u) : j0 + u;
-      s = exp2f(c * (float)lin_seg_tokens(p, len, j)) * s + own[u];
+      s = lin_decay(c, lin_seg_tokens(p, len, j))(s, own[u]);
     }
     q += U * step;
   }
@@ -239,12 +252,12 @@ __global__ void __launch_bounds__(256) lin_simt_kernel(LinPass p) {
         up[m][2] = fmaf(bw, cv.z, up[m][2]); up[m][3] = fmaf(bw, cv.w, up[m][3]);
       }
     }
-    const float wl = sm.pw[L];
+    const LinDecay wl = lin_decay(c2, L);
 #pragma unroll
     for (int m = 0; m < DA / 32; ++m) {
       float4* d = reinterpret_cast<float4*>(&sm.s[tr + 32 * m][cg]);
       const float4 v = *d;
-      *d = make_float4(fmaf(wl, v.x, up[m][0]), fmaf(wl, v.y, up[m][1]), fmaf(wl, v.z, up[m][2]), fmaf(wl, v.w, up[m][3]));
+      *d = make_float4(wl(v.x, up[m][0]), wl(v.y, up[m][1]), wl(v.z, up[m][2]), wl(v.w, up[m][3]));
     }
   }
   __syncthreads();

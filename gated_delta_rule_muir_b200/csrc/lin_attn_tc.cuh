@@ -29,10 +29,15 @@
 // parts of b: the first part is written over b once the scores are done, the
 // second beside it, the third over the first: 224 KB.
 //
-// Roles (512 threads): warp 0 issues TMA copies, warp 1 the MMAs; warps 4..7 (one
-// token row per thread) mask the scores and write outputs; warps 8..15 cut b and
-// keep the state (one row, 64 columns per thread). Hand-offs are mbarriers with
-// bounded waits:
+// Roles (768 threads): warp 0 issues TMA copies, warp 1 the MMAs; warps 4..7 (one
+// token row per thread) mask the scores and write outputs; warps 8..15 cut b (half
+// a token row per thread); warps 16..23 keep the state (one row, 64 columns per
+// thread). The products are issued y1(n), parts 1 and 2 (n), scores(n+1), part 3
+// (n), y2(n+1), so that the scores fill the wait for the third part and the
+// masking, cutting and outputs of one chunk run under the products of another.
+// The block is launched with 80 registers per thread; the warpgroups trade them
+// (64 + 96 + 2 x 64 + 2 x 96 = 6 x 80). Hand-offs are mbarriers with bounded
+// waits:
 //   full[s], empty[s]   slot s holds a tile / its last reader is done
 //   scores    scores in TMEM               (MMA -> mask, cut)
 //   weights   masked scores in TMEM        (mask -> MMA)
@@ -40,7 +45,8 @@
 //   y_free    y1 and y2 read               (mask -> MMA)
 //   cut12, cut3   parts 1 and 2 / 3 of b in shared memory (cut -> MMA)
 //   used12    parts 1 and 2 used           (MMA -> cut)
-//   ds        dS in TMEM                   (MMA -> state)
+//   ds        dS in TMEM                   (MMA -> state, cut)
+//   ds_free   dS read                      (state -> MMA)
 //   s_ready   S for the next chunk in shared memory (state -> MMA)
 #pragma once
 
@@ -50,7 +56,7 @@
 namespace muir {
 
 constexpr int kLtChunk = 128;
-constexpr int kLtThreads = 512;
+constexpr int kLtThreads = 768;
 constexpr uint32_t kLtTile = 32768, kLtBox = 16384;  // 128 rows x 128 columns bf16: two boxes of 64 columns
 // slots of the ring: with outputs five (beside S and the part tile), without six
 template <bool OUT> constexpr int kLtSlots = OUT ? 5 : 6;
@@ -82,14 +88,51 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
 }
 
-// A operand in TMEM (row = lane, two bf16 per column).
-__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t accum) {
+// One MMA with the accumulate flag known at compile time. The issuing thread must
+// not be slower than the tensor core (64 cycles for 128 x 128 x 16): with unrolled
+// steps, constant offsets added to one descriptor and constant flags a step takes
+// 65 cycles; with flags and step counts from registers it took 180 to 270.
+template <bool ACC>
+__device__ __forceinline__ void mma_step(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0)
+      : "memory");
+}
+// The same with the A operand in TMEM (row = lane, two bf16 per column).
+template <bool ACC>
+__device__ __forceinline__ void mma_step_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accum)
+      "r"(a_tmem), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0)
       : "memory");
+}
+
+// Step j of 16 channels of a K-major tile / of 16 rows of an MN-major one, in
+// descriptor units of 16 bytes.
+__host__ __device__ constexpr uint64_t lt_kstep(int j) { return (uint64_t)(((j >> 2) * kLtBox + (j & 3) * 32u) >> 4); }
+__host__ __device__ constexpr uint64_t lt_mnstep(int j) { return (uint64_t)((j * 2048u) >> 4); }
+
+template <int STEPS, bool ACC, bool A_MN, bool B_MN>
+__device__ __forceinline__ void lt_product(uint32_t d_tmem, uint32_t at, uint32_t bt, uint32_t idesc) {
+  const uint64_t a = sdesc_sw128(at, A_MN ? kLtBox : 16u, 1024u), b = sdesc_sw128(bt, B_MN ? kLtBox : 16u, 1024u);
+#pragma unroll
+  for (int j = 0; j < STEPS; ++j) {
+    const uint64_t aj = a + (A_MN ? lt_mnstep(j) : lt_kstep(j)), bj = b + (B_MN ? lt_mnstep(j) : lt_kstep(j));
+    if (ACC || j > 0) mma_step<true>(d_tmem, aj, bj, idesc);
+    else mma_step<false>(d_tmem, aj, bj, idesc);
+  }
+}
+// over 32, 64 or 128 channels
+template <bool B_MN>
+__device__ __forceinline__ void lt_product_k(int channels, uint32_t d_tmem, uint32_t at, uint32_t bt, uint32_t idesc) {
+  if (channels == 128) lt_product<8, false, false, B_MN>(d_tmem, at, bt, idesc);
+  else if (channels == 64) lt_product<4, false, false, B_MN>(d_tmem, at, bt, idesc);
+  else lt_product<2, false, false, B_MN>(d_tmem, at, bt, idesc);
 }
 
 // 16 columns (32-bit words) of this thread's lane; completes before return.
@@ -100,6 +143,31 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
+}
+
+// 32 columns from each of two places of this thread's lane: both loads, one wait.
+__device__ __forceinline__ void tmem_ld32x2(uint32_t ta, uint32_t tb, float (&a)[32], float (&b)[32]) {
+  uint32_t r[32], s[32];
+  auto issue = [](uint32_t t, uint32_t (&x)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]), "=r"(x[8]),
+          "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15]), "=r"(x[16]), "=r"(x[17]),
+          "=r"(x[18]), "=r"(x[19]), "=r"(x[20]), "=r"(x[21]), "=r"(x[22]), "=r"(x[23]), "=r"(x[24]), "=r"(x[25]), "=r"(x[26]),
+          "=r"(x[27]), "=r"(x[28]), "=r"(x[29]), "=r"(x[30]), "=r"(x[31])
+        : "r"(t)
+        : "memory");
+  };
+  issue(ta, r);
+  issue(tb, s);
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {  // after the wait: the registers are not valid before it
+    asm volatile("" : "+r"(r[i]), "+r"(s[i]));
+    a[i] = __uint_as_float(r[i]);
+    b[i] = __uint_as_float(s[i]);
+  }
 }
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
@@ -119,6 +187,16 @@ __device__ __forceinline__ void stg_bf16x16(__nv_bfloat16* p, const uint32_t (&w
     reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
+
+// One lane of a converged warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+template <int N> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // One (pass, sequence, head, segment) of a launch.
 struct LinUnit {
@@ -145,10 +223,12 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
   extern __shared__ __align__(1024) uint8_t lt_sm[];
   constexpr int SLOTS = kLtSlots<OUT>;
   constexpr int TILES = OUT ? 3 : 2;  // per chunk: a, b, c or b, c
-  __shared__ uint64_t full[SLOTS], empty[SLOTS], b_scores, b_weights, b_y, b_yfree, b_cut12, b_cut3, b_used12, b_ds, b_sready;
+  __shared__ uint64_t full[SLOTS], empty[SLOTS], b_scores, b_weights, b_y, b_yfree, b_cut12, b_cut3, b_used12, b_ds, b_dsfree, b_sready;
   __shared__ uint32_t tslot;
+  __shared__ float pw[kLtChunk];              // lambda^0 ..
+  __shared__ __align__(16) float pcol[32];    // column factors inside a block of 32 (see the mask)
   const int pi = blockIdx.y;
-  const LinPass& p = args.p[pi];
+  const LinPass p = args.p[pi];  // by value: the waits between uses would reload what a reference names
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const LinUnit u = lin_unit(p);
   const uint32_t base = (smem_u32(lt_sm) + 1023u) & ~1023u;
@@ -166,9 +246,12 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
     mbar_init(&b_cut3, 8);
     mbar_init(&b_used12, 1);
     mbar_init(&b_ds, 1);
+    mbar_init(&b_dsfree, 8);
     mbar_init(&b_sready, 8);
   }
   if (warp == 0) tmem_alloc(&tslot, 512);
+  if (tid < kLtChunk) pw[tid] = exp2f(u.c2 * (float)tid);
+  if (tid < 32) pcol[tid] = exp2f(u.c2 * (float)(p.reverse ? tid : 31 - tid));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -177,7 +260,9 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
   // chunk n of the walk: its place in the segment
   auto chunk_at = [&](int n) { return p.reverse ? u.chunks - 1 - n : n; };
 
-  if (warp == 0) {
+  if (warp < 4) {
+    regs_dec<64>();
+    if (warp == 0) {
     // ---- TMA: tiles in the order they are needed, a(n) b(n) c(n) a(n+1) .. --------
     if (lane == 0) {
       const int abytes = p.da > 64 ? 32768 : 16384, cbytes = p.dc > 64 ? 32768 : 16384;
@@ -201,79 +286,93 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       for (int s = 0; s < SLOTS; ++s)
         if (m > s) mbar_wait(&full[s], (uint32_t)((m - 1 - s) / SLOTS) & 1u);
     }
-  } else if (warp == 1) {
+    } else if (warp == 1) {
     // ---- MMA ------------------------------------------------------------------------
-    if (lane == 0) {
-      bool ok = true;
-      const int ka = p.da / 16;
-      const uint32_t id_scores = idesc_bf16(128, 128, 0, 0), id_y = idesc_bf16(128, p.dc, 0, 1),
-                     id_ds = idesc_bf16(128, p.dc, 1, 1);
-      auto part = [&](uint32_t bt, uint32_t ct, bool accum) {  // dS (+)= part^T c
-        for (int j = 0; j < 8; ++j)
-          mma_bf16(t_ds, sdesc_sw128(bt + (uint32_t)j * 2048u, kLtBox, 1024u), sdesc_sw128(ct + (uint32_t)j * 2048u, kLtBox, 1024u),
-                   id_ds, accum || j > 0 ? 1u : 0u);
-      };
-      for (int n = 0; n < u.chunks && ok; ++n) {
-        const uint32_t ph = (uint32_t)n & 1u;
-        const int m = n * TILES;
-        const int sa = m % SLOTS, sb = (m + TILES - 2) % SLOTS, sc = (m + TILES - 1) % SLOTS;
-        const uint32_t at = base + (uint32_t)sa * kLtTile, bt = base + (uint32_t)sb * kLtTile, ct = base + (uint32_t)sc * kLtTile;
-        if (OUT) {
-          ok = mbar_wait(&full[sa], (uint32_t)(m / SLOTS) & 1u) && mbar_wait(&full[sb], (uint32_t)((m + 1) / SLOTS) & 1u);
-          if (ok && n > 0) ok = mbar_wait(&b_y, ph ^ 1u);  // the last weights have been used
-          if (!ok) break;
-          tc_fence_after();
-          for (int j = 0; j < ka; ++j) {
-            const uint32_t o = (uint32_t)(j >> 2) * kLtBox + (uint32_t)(j & 3) * 32u;
-            mma_bf16(t_scores, sdesc_sw128(at + o, 16u, 1024u), sdesc_sw128(bt + o, 16u, 1024u), id_scores, j > 0 ? 1u : 0u);
-          }
-          mma_commit(&b_scores);
-          ok = mbar_wait(&b_sready, ph);
-          if (ok && n > 0) ok = mbar_wait(&b_yfree, ph ^ 1u);
-          if (!ok) break;
-          tc_fence_after();
-          for (int j = 0; j < ka; ++j) {
-            const uint32_t o = (uint32_t)(j >> 2) * kLtBox + (uint32_t)(j & 3) * 32u;
-            mma_bf16(t_y2, sdesc_sw128(at + o, 16u, 1024u), sdesc_sw128(s_tile + (uint32_t)j * 2048u, kLtBox, 1024u), id_y,
-                     j > 0 ? 1u : 0u);
-          }
-          mma_commit(&empty[sa]);
-        }
-        ok = mbar_wait(&full[sc], (uint32_t)((m + TILES - 1) / SLOTS) & 1u) && mbar_wait(&b_cut12, ph);
+    // The warp stays converged and one elected lane issues: slots, step counts and
+    // waits' results are the same in every lane and known to be (a vote, a warp
+    // reduction), so that the descriptors are formed in uniform registers. Issued
+    // from inside a one-lane branch, each product took three to four times as long.
+    const bool leader = elect_one();
+    const int chunks = (int)__reduce_max_sync(0xffffffffu, (unsigned)u.chunks);
+    const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
+    const uint32_t m_scores = tm, m_y1 = tm + 128, m_y2 = tm + 256, m_ds = tm + 384;
+    bool ok = true;
+    const uint32_t id_scores = idesc_bf16(128, 128, 0, 0), id_y = idesc_bf16(128, p.dc, 0, 1),
+                   id_ds = idesc_bf16(128, p.dc, 1, 1);
+    auto slot = [&](int m) { return base + (uint32_t)(m % SLOTS) * kLtTile; };
+    auto landed = [&](int m) { return warp_wait(&full[m % SLOTS], (uint32_t)(m / SLOTS) & 1u); };
+    auto scores = [&](int n) {  // a b^T of chunk n; its TMEM columns hold chunk n - 1's weights until y1 is done
+      const int m = n * TILES;
+      if (!landed(m) || !landed(m + 1) || (n > 0 && !warp_wait(&b_y, (uint32_t)(n - 1) & 1u))) return false;
+      tc_fence_after();
+      if (leader) {
+        lt_product_k<false>(p.da, m_scores, slot(m), slot(m + 1), id_scores);
+        mma_commit(&b_scores);
+      }
+      __syncwarp();
+      return true;
+    };
+    if (OUT && chunks > 0) ok = scores(0);
+    for (int n = 0; n < chunks && ok; ++n) {
+      const uint32_t ph = (uint32_t)n & 1u;
+      const int ma = n * TILES, mb = ma + TILES - 2, mc = ma + TILES - 1;
+      const uint32_t at = slot(ma), bt = slot(mb), ct = slot(mc);
+      if (OUT) {
+        ok = warp_wait(&b_sready, ph) && (n == 0 || warp_wait(&b_yfree, ph ^ 1u));
         if (!ok) break;
         tc_fence_after();
-        part(bt, ct, false);
-        part(x_tile, ct, true);
-        mma_commit(&b_used12);
+        if (leader) {
+          lt_product_k<true>(p.da, m_y2, at, s_tile, id_y);
+          mma_commit(&empty[ma % SLOTS]);
+        }
+        __syncwarp();
+      }
+      // c's tile: landed, and its rows past the last token cleared by the cutters
+      ok = landed(mc) && warp_wait(&b_cut12, ph);
+      if (OUT) ok = ok && warp_wait(&b_weights, ph);
+      if (n > 0) ok = ok && warp_wait(&b_dsfree, ph ^ 1u);
+      if (!ok) break;
+      tc_fence_after();
+      if (leader) {
         if (OUT) {
-          ok = mbar_wait(&b_weights, ph);
-          if (!ok) break;
-          tc_fence_after();
-          for (int j = 0; j < 8; ++j)
-            mma_bf16_ta(t_y1, t_scores + (uint32_t)j * 8u, sdesc_sw128(ct + (uint32_t)j * 2048u, kLtBox, 1024u), id_y,
-                        j > 0 ? 1u : 0u);
+          const uint64_t cd = sdesc_sw128(ct, kLtBox, 1024u);
+          mma_step_ta<false>(m_y1, m_scores, cd, id_y);
+#pragma unroll
+          for (int j = 1; j < 8; ++j) mma_step_ta<true>(m_y1, m_scores + (uint32_t)j * 8u, cd + lt_mnstep(j), id_y);
           mma_commit(&b_y);
         }
-        ok = mbar_wait(&b_cut3, ph);
-        if (!ok) break;
-        tc_fence_after();
-        part(bt, ct, true);
-        mma_commit(&empty[sb]);
-        mma_commit(&empty[sc]);
+        lt_product<8, false, true, true>(m_ds, bt, ct, id_ds);
+        lt_product<8, true, true, true>(m_ds, x_tile, ct, id_ds);
+        mma_commit(&b_used12);
+      }
+      __syncwarp();
+      if (OUT && n + 1 < chunks) ok = scores(n + 1);
+      ok = ok && warp_wait(&b_cut3, ph);
+      if (!ok) break;
+      tc_fence_after();
+      if (leader) {
+        lt_product<8, true, true, true>(m_ds, bt, ct, id_ds);
+        mma_commit(&empty[mb % SLOTS]);
+        mma_commit(&empty[mc % SLOTS]);
         mma_commit(&b_ds);
       }
-      // every issued product has completed when the CTA ends: each chunk's last commit
-      // is waited for here, or after a wait that ran out one more commit is
-      if (ok) {
-        if (u.chunks > 0) mbar_wait(&b_ds, (uint32_t)(u.chunks - 1) & 1u);
-      } else {
-        mma_commit(&b_ds);
-        mbar_wait_for(&b_ds, 0u, 1000000ull);
-        mbar_wait_for(&b_ds, 1u, 1000000ull);
-      }
+      __syncwarp();
     }
-  } else if (OUT && warp >= 4 && warp < 8) {
+    // every issued product has completed when the CTA ends: the last chunk's commit
+    // is waited for here, or after a wait that ran out one more commit is
+    if (ok) {
+      if (chunks > 0) warp_wait(&b_ds, (uint32_t)(chunks - 1) & 1u);
+    } else {
+      if (leader) mma_commit(&b_ds);
+      __syncwarp();
+      mbar_wait_for(&b_ds, 0u, 1000000ull);
+      mbar_wait_for(&b_ds, 1u, 1000000ull);
+    }
+    }
+  } else if (warp < 8) {
     // ---- mask and outputs: thread = token row i of the chunk ----------------------------
+    regs_inc<96>();
+    if constexpr (OUT) {
     const int w = warp & 3, i = w * 32 + lane;
     const uint32_t row = tmem_lane_base(warp);
     __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(p.out) + (((int64_t)u.b * p.T + u.t0) * p.H + u.h) * p.dc;
@@ -286,9 +385,6 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
     }
     // lambda^gap = (row factor of a block of 32 columns) (column factor in the block),
     // both at most 1 for blocks off the diagonal
-    float cf[32];
-#pragma unroll
-    for (int s = 0; s < 32; ++s) cf[s] = exp2f(u.c2 * (float)(p.reverse ? s : 31 - s));
     bool ok = true;
     for (int n = 0; n < u.chunks && ok; ++n) {
       const uint32_t ph = (uint32_t)n & 1u;
@@ -308,19 +404,32 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
           float v[32];
           tmem_ld32(t_scores + row + (uint32_t)(32 * k), v);
           if (k == w) {
+            const int last = L - 32 * k;  // columns from here on are past the last token
 #pragma unroll
             for (int s = 0; s < 32; ++s) {
               const int gap = p.reverse ? s - lane : lane - s;
+              const float f = v[s] * (p.p_scale * pw[gap & 31]);
               // dropped, not multiplied by zero: a masked score may be anything
-              v[s] = gap >= 0 && 32 * k + s < L ? v[s] * (p.p_scale * exp2f(u.c2 * (float)gap)) : 0.f;
+              v[s] = (gap >= 0) & (s < last) ? f : 0.f;
             }
+#pragma unroll
+            for (int q = 0; q < 16; ++q) wd[q] = bf16x2(v[2 * q], v[2 * q + 1]);
           } else {
-            const float rf = p.p_scale * exp2f(u.c2 * (float)(p.reverse ? 32 * k - i : i - 32 * k - 31));
+            const float rf = p.p_scale * pw[p.reverse ? 32 * k - i : i - 32 * k - 31];
+            const float2 rf2 = make_float2(rf, rf);
+            if (32 * k + 32 > L) {  // columns past the last token
 #pragma unroll
-            for (int s = 0; s < 32; ++s) v[s] = 32 * k + s < L ? v[s] * (rf * cf[s]) : 0.f;
+              for (int s = 0; s < 32; ++s) v[s] = 32 * k + s < L ? v[s] : 0.f;
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const float4 cf = *reinterpret_cast<const float4*>(&pcol[4 * q]);
+              const float2 f = __fmul2_rn(make_float2(v[4 * q], v[4 * q + 1]), __fmul2_rn(make_float2(cf.x, cf.y), rf2));
+              const float2 g = __fmul2_rn(make_float2(v[4 * q + 2], v[4 * q + 3]), __fmul2_rn(make_float2(cf.z, cf.w), rf2));
+              wd[2 * q] = bf16x2(f.x, f.y);
+              wd[2 * q + 1] = bf16x2(g.x, g.y);
+            }
           }
-#pragma unroll
-          for (int q = 0; q < 16; ++q) wd[q] = bf16x2(v[2 * q], v[2 * q + 1]);
         }
         // columns 16 k .. of the scores have been read: block k's weights go there
         tmem_st16(t_scores + row + (uint32_t)(16 * k), wd);
@@ -331,12 +440,11 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       ok = warp_wait(&b_y, ph);
       if (!ok) break;
       tc_fence_after();
-      const float rw = p.o_scale * exp2f(u.c2 * (float)(p.reverse ? (i < L ? L - 1 - i : 0) : i + 1));
+      const float rw = p.o_scale * (p.reverse ? pw[i < L ? L - 1 - i : 0] : exp2f(u.c2 * (float)(i + 1)));
 #pragma unroll 1
       for (int c = 0; c < p.dc; c += 32) {
         float y1[32], y2[32];
-        tmem_ld32(t_y1 + row + (uint32_t)c, y1);
-        tmem_ld32(t_y2 + row + (uint32_t)c, y2);
+        tmem_ld32x2(t_y1 + row + (uint32_t)c, t_y2 + row + (uint32_t)c, y1, y2);
         if (c + 32 >= p.dc) {
           tc_fence_before();
           __syncwarp();
@@ -348,21 +456,100 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
           for (int hf = 0; hf < 2; ++hf) {
             uint32_t o[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-              o[q] = bf16x2(fmaf(rw, y2[16 * hf + 2 * q], y1[16 * hf + 2 * q]),
-                            fmaf(rw, y2[16 * hf + 2 * q + 1], y1[16 * hf + 2 * q + 1]));
+            for (int q = 0; q < 8; ++q) {
+              const int e = 16 * hf + 2 * q;
+              const float2 y = __ffma2_rn(make_float2(rw, rw), make_float2(y2[e], y2[e + 1]), make_float2(y1[e], y1[e + 1]));
+              o[q] = bf16x2(y.x, y.y);
+            }
             stg_bf16x16(d + 16 * hf, o);
           }
         }
       }
     }
-  } else if (warp >= 8) {
-    // ---- cut b, keep the state ------------------------------------------------------------
-    const int half = (warp - 8) >> 2;            // columns 64 half .. of b's tile and of S
-    const int r = (warp & 3) * 32 + lane;        // token row of b's tile; row of S
+    }
+  } else if (warp < 16) {
+    // ---- cut b: thread = half a token row ---------------------------------------------------
+    regs_dec<64>();
+    const int half = (warp - 8) >> 2;      // columns 64 half ..
+    const int r = (warp & 3) * 32 + lane;  // token row
+    const int bcols = p.da - 64 * half < 64 ? p.da - 64 * half : 64;  // at most 0: none
+    const uint32_t place = (uint32_t)half * kLtBox + (uint32_t)r * 128u;
+    bool ok = true;
+    for (int n = 0; n < u.chunks && ok; ++n) {
+      const uint32_t ph = (uint32_t)n & 1u;
+      const int64_t r0 = (int64_t)chunk_at(n) * kLtChunk;
+      const int L = (int)(u.valid - r0 < kLtChunk ? u.valid - r0 : kLtChunk);
+      const int m = n * TILES + TILES - 2;
+      const int sb = m % SLOTS, sc = (m + 1) % SLOTS;
+      const uint32_t line = base + (uint32_t)sb * kLtTile + place;
+      const uint32_t xline = x_tile + place;
+      const float wt = r < L ? p.u_scale * exp2f(u.c2 * (float)(p.reverse ? r + 1 : L - 1 - r)) : 0.f;
+      ok = warp_wait(&full[sb], (uint32_t)(m / SLOTS) & 1u) && warp_wait(&full[sc], (uint32_t)((m + 1) / SLOTS) & 1u);
+      if (OUT && ok) ok = warp_wait(&b_scores, ph);  // b itself has been used
+      if (ok && n > 0) ok = warp_wait(&b_used12, ph ^ 1u);  // and the last second part
+      if (!ok) break;
+      uint32_t x[32];  // the half row, then its third parts
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const uint4 v = *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(line + (uint32_t)((c ^ (r & 7)) << 4)));
+        // rows past the last token count as zeros, whatever they hold
+        x[4 * c] = r < L ? v.x : 0u;
+        x[4 * c + 1] = r < L ? v.y : 0u;
+        x[4 * c + 2] = r < L ? v.z : 0u;
+        x[4 * c + 3] = r < L ? v.w : 0u;
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        uint32_t p1[4], p2[4];
+        const float2 minus = make_float2(-1.f, -1.f);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t in = x[4 * c + q];
+          float2 f = __fmul2_rn(make_float2(__uint_as_float(in << 16), __uint_as_float(in & 0xFFFF0000u)), make_float2(wt, wt));
+          auto upper = [&]() {
+            return make_float2(__uint_as_float(__float_as_uint(f.x) & 0xFFFF0000u),
+                               __uint_as_float(__float_as_uint(f.y) & 0xFFFF0000u));
+          };
+          auto pack = [&]() { return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632); };
+          p1[q] = pack();
+          f = __ffma2_rn(upper(), minus, f);
+          p2[q] = pack();
+          f = __ffma2_rn(upper(), minus, f);
+          x[4 * c + q] = pack();
+        }
+        if (8 * c < bcols) {
+          const uint32_t at = (uint32_t)((c ^ (r & 7)) << 4);
+          sts128(line + at, make_uint4(p1[0], p1[1], p1[2], p1[3]));
+          sts128(xline + at, make_uint4(p2[0], p2[1], p2[2], p2[3]));
+        }
+      }
+      if (r >= L) {  // c's rows past the last token: zero times anything must stay zero
+        const uint32_t cline = base + (uint32_t)sc * kLtTile + place;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) sts128(cline + (uint32_t)(c << 4), make_uint4(0u, 0u, 0u, 0u));
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive1(&b_cut12);
+      ok = warp_wait(&b_used12, ph);
+      if (!ok) break;
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (8 * c < bcols)
+          sts128(line + (uint32_t)((c ^ (r & 7)) << 4),
+                 make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]));
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive1(&b_cut3);
+    }
+  } else {
+    // ---- the state: thread = row r, columns 64 half .. -----------------------------------------
+    regs_inc<96>();
+    const int half = (warp - 16) >> 2;
+    const int r = (warp & 3) * 32 + lane;
     const uint32_t row = tmem_lane_base(warp);
     const int nstate = p.da * p.dc;
-    const bool mine = r < p.da && 64 * half < p.dc;       // has a row of S
+    const bool mine = r < p.da && 64 * half < p.dc;
     const int scols = p.dc - 64 * half < 64 ? p.dc - 64 * half : 64;
     float S[64];
     {
@@ -379,7 +566,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
           S[j] = tr ? __ldg(src + (int64_t)(64 * half + j) * p.da + r) : __ldg(src + (int64_t)r * p.dc + 64 * half + j);
       }
     }
-    auto put_state = [&]() {  // S's operand copy: row r, columns 64 half ..
+    auto put_state = [&]() {  // S's operand copy
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         if (mine && 8 * c < scols) {
@@ -396,78 +583,33 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       if (lane == 0) mbar_arrive1(&b_sready);
     };
     if constexpr (OUT) put_state();
-    const int bcols = p.da - 64 * half < 64 ? p.da - 64 * half : 64;  // of b's tile, at most 0: none
     bool ok = true;
     for (int n = 0; n < u.chunks && ok; ++n) {
-      const uint32_t ph = (uint32_t)n & 1u;
       const int64_t r0 = (int64_t)chunk_at(n) * kLtChunk;
       const int L = (int)(u.valid - r0 < kLtChunk ? u.valid - r0 : kLtChunk);
-      const int m = n * TILES + TILES - 2;
-      const int sb = m % SLOTS, sc = (m + 1) % SLOTS;
-      const uint32_t line = base + (uint32_t)sb * kLtTile + (uint32_t)half * kLtBox + (uint32_t)r * 128u;
-      const uint32_t xline = x_tile + (uint32_t)half * kLtBox + (uint32_t)r * 128u;
-      const float wt = r < L ? p.u_scale * exp2f(u.c2 * (float)(p.reverse ? r + 1 : L - 1 - r)) : 0.f;
-      ok = warp_wait(&full[sb], (uint32_t)(m / SLOTS) & 1u) && warp_wait(&full[sc], (uint32_t)((m + 1) / SLOTS) & 1u);
-      if (OUT && ok) ok = warp_wait(&b_scores, ph);  // b itself has been used
-      if (!ok) break;
-      uint32_t third[32];
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const uint32_t at = (uint32_t)((c ^ (r & 7)) << 4);
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (8 * c < bcols) v = *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(line + at));
-        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-        uint32_t p1[4], p2[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          // rows past the last token become zeros whatever they hold
-          float f0 = r < L ? __uint_as_float(in[q] << 16) * wt : 0.f;
-          float f1 = r < L ? __uint_as_float(in[q] & 0xFFFF0000u) * wt : 0.f;
-          p1[q] = __byte_perm(__float_as_uint(f0), __float_as_uint(f1), 0x7632);
-          f0 -= __uint_as_float(__float_as_uint(f0) & 0xFFFF0000u);
-          f1 -= __uint_as_float(__float_as_uint(f1) & 0xFFFF0000u);
-          p2[q] = __byte_perm(__float_as_uint(f0), __float_as_uint(f1), 0x7632);
-          f0 -= __uint_as_float(__float_as_uint(f0) & 0xFFFF0000u);
-          f1 -= __uint_as_float(__float_as_uint(f1) & 0xFFFF0000u);
-          third[4 * c + q] = __byte_perm(__float_as_uint(f0), __float_as_uint(f1), 0x7632);
-        }
-        if (8 * c < bcols) {
-          sts128(line + at, make_uint4(p1[0], p1[1], p1[2], p1[3]));
-          sts128(xline + at, make_uint4(p2[0], p2[1], p2[2], p2[3]));
-        }
-      }
-      if (r >= L) {  // c's rows past the last token: zero times anything must stay zero
-        const uint32_t cline = base + (uint32_t)sc * kLtTile + (uint32_t)half * kLtBox + (uint32_t)r * 128u;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) sts128(cline + (uint32_t)(c << 4), make_uint4(0u, 0u, 0u, 0u));
-      }
-      fence_async_smem();
-      tc_fence_before();  // this thread's reads of the last dS precede the next
-      __syncwarp();
-      if (lane == 0) mbar_arrive1(&b_cut12);
-      ok = warp_wait(&b_used12, ph);
-      if (!ok) break;
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-        if (8 * c < bcols)
-          sts128(line + (uint32_t)((c ^ (r & 7)) << 4),
-                 make_uint4(third[4 * c], third[4 * c + 1], third[4 * c + 2], third[4 * c + 3]));
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive1(&b_cut3);
-      ok = warp_wait(&b_ds, ph);
+      const LinDecay wl = lin_decay(u.c2, L);
+      ok = warp_wait(&b_ds, (uint32_t)n & 1u);
       if (!ok) break;
       tc_fence_after();
-      const float wl = exp2f(u.c2 * (float)L);
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        if (64 * half + 32 * hf < p.dc) {  // whole warps
+      for (int q = 0; q < 2; ++q) {
+        if (64 * half + 32 * q < p.dc) {  // whole warps
           float d[32];
-          tmem_ld32(t_ds + row + (uint32_t)(64 * half + 32 * hf), d);
+          tmem_ld32(t_ds + row + (uint32_t)(64 * half + 32 * q), d);
+          const float2 g = make_float2(wl.g, wl.g), e = make_float2(wl.e, wl.e);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) S[32 * hf + j] = fmaf(wl, S[32 * hf + j], d[j]);
+          for (int j = 0; j < 32; j += 2) {
+            float* s2 = S + 32 * q + j;
+            const float2 old = make_float2(s2[0], s2[1]);
+            const float2 now = __ffma2_rn(g, old, __ffma2_rn(e, old, make_float2(d[j], d[j + 1])));
+            s2[0] = now.x;
+            s2[1] = now.y;
+          }
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive1(&b_dsfree);
       if (OUT && n + 1 < u.chunks) put_state();
     }
     float* dst = nullptr;
