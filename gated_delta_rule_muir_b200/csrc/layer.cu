@@ -148,7 +148,7 @@ int lin_simt_pass(const muir::LinPass& p, int dtype, bool out, const char* name,
   return out ? lin_simt_da<float, true>(p, name, s) : lin_simt_da<float, false>(p, name, s);
 }
 
-template <bool OUT>
+template <bool OUT, int PARTS>
 int lin_tc(const muir::LinPass* p, int n, const char* name, cudaStream_t s) {
   muir::LinTcArgs args{};
   for (int i = 0; i < n; ++i) {
@@ -162,9 +162,9 @@ int lin_tc(const muir::LinPass* p, int n, const char* name, cudaStream_t s) {
   }
   const int64_t blocks = (int64_t)p->B * p->H * p->nseg;
   if (blocks > kMaxBlocks) return fail(MUIR_ERR_UNSUPPORTED, "%s: too many blocks", name);
-  if (int rc = set_smem(muir::lin_tc_kernel<OUT>, muir::kLtSmem)) return rc;
+  if (int rc = set_smem(muir::lin_tc_kernel<OUT, PARTS>, muir::kLtSmem)) return rc;
   LaunchScope l(name, s);
-  muir::lin_tc_kernel<OUT><<<dim3((unsigned)blocks, (unsigned)n), muir::kLtThreads, muir::kLtSmem, s>>>(args);
+  muir::lin_tc_kernel<OUT, PARTS><<<dim3((unsigned)blocks, (unsigned)n), muir::kLtThreads, muir::kLtSmem, s>>>(args);
   return check_launch(name);
 }
 
@@ -175,7 +175,7 @@ int lin_run(const LinPlan& pl, int dtype, const muir::LinPass* states, int ns, c
   int rc = MUIR_OK;
   if (pl.nseg > 1) {
     if (pl.tc) {
-      if ((rc = lin_tc<false>(states, ns, "lin_state", s))) return rc;
+      if ((rc = lin_tc<false, 3>(states, ns, "lin_state", s))) return rc;
     } else {
       for (int i = 0; i < ns; ++i)
         if ((rc = lin_simt_pass(states[i], dtype, false, "lin_state", s))) return rc;
@@ -187,7 +187,12 @@ int lin_run(const LinPlan& pl, int dtype, const muir::LinPass* states, int ns, c
     muir::lin_combine_kernel<<<dim3((unsigned)(p.da * p.dc / 128), (unsigned)(p.B * p.H), (unsigned)ns), 128, 0, s>>>(ca);
     if ((rc = check_launch("lin_combine"))) return rc;
   }
-  if (pl.tc) return lin_tc<true>(outs, no, name, s);
+  if (pl.tc) {
+    // a final state comes from this launch only where there is one segment
+    bool fin = false;
+    for (int i = 0; i < no; ++i) fin = fin || (pl.nseg == 1 && outs[i].fin);
+    return fin ? lin_tc<true, 3>(outs, no, name, s) : lin_tc<true, 2>(outs, no, name, s);
+  }
   for (int i = 0; i < no; ++i)
     if ((rc = lin_simt_pass(outs[i], dtype, true, name, s))) return rc;
   return MUIR_OK;

@@ -58,8 +58,7 @@ namespace muir {
 constexpr int kLtChunk = 128;
 constexpr int kLtThreads = 768;
 constexpr uint32_t kLtTile = 32768, kLtBox = 16384;  // 128 rows x 128 columns bf16: two boxes of 64 columns
-// slots of the ring: with outputs five (beside S and the part tile), without six
-template <bool OUT> constexpr int kLtSlots = OUT ? 5 : 6;
+constexpr int kLtSlots = 5;
 constexpr uint32_t kLtSmem = 7 * kLtTile + 1024;
 
 constexpr int kLinMaxPasses = 3;
@@ -218,12 +217,12 @@ __device__ __forceinline__ LinUnit lin_unit(const LinPass& p) {
   return u;
 }
 
-template <bool OUT>
+template <bool OUT, int PARTS>
 __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_constant__ LinTcArgs args) {
   extern __shared__ __align__(1024) uint8_t lt_sm[];
-  constexpr int SLOTS = kLtSlots<OUT>;
+  constexpr int SLOTS = kLtSlots;
   constexpr int TILES = OUT ? 3 : 2;  // per chunk: a, b, c or b, c
-  __shared__ uint64_t full[SLOTS], empty[SLOTS], b_scores, b_weights, b_y, b_yfree, b_cut12, b_cut3, b_used12, b_ds, b_dsfree, b_sready;
+  __shared__ uint64_t full[SLOTS], empty[SLOTS], b_scores, b_weights, b_y2, b_y, b_yfree, b_cut12, b_cut3, b_used12, b_ds, b_dsfree, b_sready;
   __shared__ uint32_t tslot;
   __shared__ float pw[kLtChunk];              // lambda^0 ..
   __shared__ __align__(16) float pcol[32];    // column factors inside a block of 32 (see the mask)
@@ -232,7 +231,9 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const LinUnit u = lin_unit(p);
   const uint32_t base = (smem_u32(lt_sm) + 1023u) & ~1023u;
-  const uint32_t s_tile = base + 5u * kLtTile, x_tile = base + 6u * kLtTile;  // without outputs s_tile is slot 5
+  // beside the ring: the second parts' tile, and S's or (without outputs) a second one
+  const uint32_t x_tile = base + 5u * kLtTile, s_tile = base + 6u * kLtTile;
+  auto x_of = [&](int n) { return OUT ? x_tile : x_tile + (uint32_t)(n & 1) * kLtTile; };
   if (tid == 0) {
     for (int i = 0; i < SLOTS; ++i) {
       mbar_init(&full[i], 1);
@@ -240,6 +241,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
     }
     mbar_init(&b_scores, 1);
     mbar_init(&b_weights, 4);
+    mbar_init(&b_y2, 1);
     mbar_init(&b_y, 1);
     mbar_init(&b_yfree, 4);
     mbar_init(&b_cut12, 8);
@@ -317,51 +319,63 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       const uint32_t ph = (uint32_t)n & 1u;
       const int ma = n * TILES, mb = ma + TILES - 2, mc = ma + TILES - 1;
       const uint32_t at = slot(ma), bt = slot(mb), ct = slot(mc);
+      // c's tile: landed, and its rows past the last token cleared by the cutters
+      ok = landed(mc) && warp_wait(&b_cut12, ph) && (n == 0 || warp_wait(&b_dsfree, ph ^ 1u));
+      if (!ok) break;
+      tc_fence_after();
+      if (leader) {
+        lt_product<8, false, true, true>(m_ds, bt, ct, id_ds);
+        lt_product<8, true, true, true>(m_ds, x_of(n), ct, id_ds);
+        mma_commit(PARTS == 2 ? &b_ds : &b_used12);
+      }
+      __syncwarp();
       if (OUT) {
         ok = warp_wait(&b_sready, ph) && (n == 0 || warp_wait(&b_yfree, ph ^ 1u));
         if (!ok) break;
         tc_fence_after();
         if (leader) {
           lt_product_k<true>(p.da, m_y2, at, s_tile, id_y);
+          mma_commit(&b_y2);
           mma_commit(&empty[ma % SLOTS]);
         }
         __syncwarp();
-      }
-      // c's tile: landed, and its rows past the last token cleared by the cutters
-      ok = landed(mc) && warp_wait(&b_cut12, ph);
-      if (OUT) ok = ok && warp_wait(&b_weights, ph);
-      if (n > 0) ok = ok && warp_wait(&b_dsfree, ph ^ 1u);
-      if (!ok) break;
-      tc_fence_after();
-      if (leader) {
-        if (OUT) {
+        ok = warp_wait(&b_weights, ph);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
           const uint64_t cd = sdesc_sw128(ct, kLtBox, 1024u);
           mma_step_ta<false>(m_y1, m_scores, cd, id_y);
 #pragma unroll
           for (int j = 1; j < 8; ++j) mma_step_ta<true>(m_y1, m_scores + (uint32_t)j * 8u, cd + lt_mnstep(j), id_y);
           mma_commit(&b_y);
+          if (PARTS == 2) {
+            mma_commit(&empty[mb % SLOTS]);
+            mma_commit(&empty[mc % SLOTS]);
+          }
         }
-        lt_product<8, false, true, true>(m_ds, bt, ct, id_ds);
-        lt_product<8, true, true, true>(m_ds, x_tile, ct, id_ds);
-        mma_commit(&b_used12);
+        __syncwarp();
+        if (n + 1 < chunks) ok = scores(n + 1);
       }
-      __syncwarp();
-      if (OUT && n + 1 < chunks) ok = scores(n + 1);
-      ok = ok && warp_wait(&b_cut3, ph);
-      if (!ok) break;
-      tc_fence_after();
-      if (leader) {
-        lt_product<8, true, true, true>(m_ds, bt, ct, id_ds);
-        mma_commit(&empty[mb % SLOTS]);
-        mma_commit(&empty[mc % SLOTS]);
-        mma_commit(&b_ds);
+      if (PARTS == 3) {
+        ok = ok && warp_wait(&b_cut3, ph);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          lt_product<8, true, true, true>(m_ds, bt, ct, id_ds);
+          mma_commit(&b_ds);
+          mma_commit(&empty[mb % SLOTS]);
+          mma_commit(&empty[mc % SLOTS]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
-    // every issued product has completed when the CTA ends: the last chunk's commit
-    // is waited for here, or after a wait that ran out one more commit is
+    // every issued product has completed when the CTA ends: the last chunk's commits
+    // are waited for here, or after a wait that ran out one more commit is
     if (ok) {
-      if (chunks > 0) warp_wait(&b_ds, (uint32_t)(chunks - 1) & 1u);
+      if (chunks > 0) {
+        warp_wait(&b_ds, (uint32_t)(chunks - 1) & 1u);
+        if (OUT) warp_wait(&b_y, (uint32_t)(chunks - 1) & 1u);
+      }
     } else {
       if (leader) mma_commit(&b_ds);
       __syncwarp();
@@ -482,21 +496,26 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       const int m = n * TILES + TILES - 2;
       const int sb = m % SLOTS, sc = (m + 1) % SLOTS;
       const uint32_t line = base + (uint32_t)sb * kLtTile + place;
-      const uint32_t xline = x_tile + place;
+      const uint32_t xline = x_of(n) + place;
       const float wt = r < L ? p.u_scale * exp2f(u.c2 * (float)(p.reverse ? r + 1 : L - 1 - r)) : 0.f;
       ok = warp_wait(&full[sb], (uint32_t)(m / SLOTS) & 1u) && warp_wait(&full[sc], (uint32_t)((m + 1) / SLOTS) & 1u);
-      if (OUT && ok) ok = warp_wait(&b_scores, ph);  // b itself has been used
-      if (ok && n > 0) ok = warp_wait(&b_used12, ph ^ 1u);  // and the last second part
+      if (OUT) {
+        ok = ok && warp_wait(&b_scores, ph);  // b itself has been used, and the last second parts
+        if (PARTS == 2 && n > 0) ok = ok && warp_wait(&b_ds, ph ^ 1u);
+      }
       if (!ok) break;
       uint32_t x[32];  // the half row, then its third parts
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         const uint4 v = *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(line + (uint32_t)((c ^ (r & 7)) << 4)));
-        // rows past the last token count as zeros, whatever they hold
-        x[4 * c] = r < L ? v.x : 0u;
-        x[4 * c + 1] = r < L ? v.y : 0u;
-        x[4 * c + 2] = r < L ? v.z : 0u;
-        x[4 * c + 3] = r < L ? v.w : 0u;
+        x[4 * c] = v.x;
+        x[4 * c + 1] = v.y;
+        x[4 * c + 2] = v.z;
+        x[4 * c + 3] = v.w;
+      }
+      if (r >= L) {  // rows past the last token count as zeros, whatever they hold
+#pragma unroll
+        for (int c = 0; c < 32; ++c) x[c] = 0u;
       }
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
@@ -506,16 +525,22 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
         for (int q = 0; q < 4; ++q) {
           const uint32_t in = x[4 * c + q];
           float2 f = __fmul2_rn(make_float2(__uint_as_float(in << 16), __uint_as_float(in & 0xFFFF0000u)), make_float2(wt, wt));
-          auto upper = [&]() {
-            return make_float2(__uint_as_float(__float_as_uint(f.x) & 0xFFFF0000u),
-                               __uint_as_float(__float_as_uint(f.y) & 0xFFFF0000u));
-          };
-          auto pack = [&]() { return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632); };
-          p1[q] = pack();
-          f = __ffma2_rn(upper(), minus, f);
-          p2[q] = pack();
-          f = __ffma2_rn(upper(), minus, f);
-          x[4 * c + q] = pack();
+          if (PARTS == 2) {
+            p1[q] = bf16x2(f.x, f.y);
+            f = __ffma2_rn(make_float2(__uint_as_float(p1[q] << 16), __uint_as_float(p1[q] & 0xFFFF0000u)), minus, f);
+            p2[q] = bf16x2(f.x, f.y);
+          } else {
+            auto upper = [&]() {
+              return make_float2(__uint_as_float(__float_as_uint(f.x) & 0xFFFF0000u),
+                                 __uint_as_float(__float_as_uint(f.y) & 0xFFFF0000u));
+            };
+            auto pack = [&]() { return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632); };
+            p1[q] = pack();
+            f = __ffma2_rn(upper(), minus, f);
+            p2[q] = pack();
+            f = __ffma2_rn(upper(), minus, f);
+            x[4 * c + q] = pack();
+          }
         }
         if (8 * c < bcols) {
           const uint32_t at = (uint32_t)((c ^ (r & 7)) << 4);
@@ -531,16 +556,17 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive1(&b_cut12);
-      ok = warp_wait(&b_used12, ph);
-      if (!ok) break;
+      if (PARTS == 3) {
+        ok = warp_wait(&b_used12, ph);
+        if (!ok) break;
 #pragma unroll
-      for (int c = 0; c < 8; ++c)
-        if (8 * c < bcols)
-          sts128(line + (uint32_t)((c ^ (r & 7)) << 4),
-                 make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]));
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive1(&b_cut3);
+        for (int c = 0; c < 8; ++c)
+          if (8 * c < bcols)
+            sts128(line + (uint32_t)((c ^ (r & 7)) << 4), make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]));
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive1(&b_cut3);
+      }
     }
   } else {
     // ---- the state: thread = row r, columns 64 half .. -----------------------------------------
@@ -610,7 +636,11 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive1(&b_dsfree);
-      if (OUT && n + 1 < u.chunks) put_state();
+      if (OUT && n + 1 < u.chunks) {
+        ok = warp_wait(&b_y2, (uint32_t)n & 1u);  // the last copy has been used
+        if (!ok) break;
+        put_state();
+      }
     }
     float* dst = nullptr;
     if constexpr (!OUT) dst = p.seg + ((int64_t)u.bh * p.nseg + u.seg) * nstate;

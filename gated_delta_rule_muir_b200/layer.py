@@ -8,7 +8,6 @@ operands' device); what a call allocates is allocated for that stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 
 import torch
@@ -16,18 +15,20 @@ import torch
 from . import _native as N
 
 _E4M3 = torch.float8_e4m3fn
+# handle of a device's current stream (a tenth of a microsecond; building a Stream object takes three)
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _ptr(t):
-    return None if t is None else C.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _need(t, name, shape, dtype, device):
-    if not isinstance(t, torch.Tensor):
+    if type(t) is not torch.Tensor and not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a tensor, got {type(t).__name__}")
-    if t.shape != torch.Size(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name}: must be a contiguous CUDA tensor")
@@ -48,17 +49,35 @@ def _io_code(t, name):
     return code
 
 
-@contextlib.contextmanager
-def _on(device, stream):
-    """The operands' device and the launch stream made current, for allocations and launches."""
-    if device.type != "cuda":
-        raise ValueError(f"operands must be CUDA tensors, got {device}")
-    with torch.cuda.device(device):
-        s = torch.cuda.current_stream() if stream is None else stream
-        if s.device != device:
-            raise ValueError(f"stream of {s.device}, operands on {device}")
-        with torch.cuda.stream(s):
-            yield C.c_void_p(s.cuda_stream)
+class _On:
+    """The operands' device and the launch stream made current, for allocations and launches;
+    gives the stream's handle. The common call (the current device and its current stream)
+    switches nothing."""
+
+    __slots__ = ("device", "stream", "guards")
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.guards = device, stream, ()
+
+    def __enter__(self):
+        device, stream = self.device, self.stream
+        if device.type != "cuda":
+            raise ValueError(f"operands must be CUDA tensors, got {device}")
+        if stream is None:
+            if device.index == torch.cuda.current_device():
+                return _raw_stream(device.index)
+            stream = torch.cuda.current_stream(device)
+        elif stream.device != device:
+            raise ValueError(f"stream of {stream.device}, operands on {device}")
+        self.guards = (torch.cuda.device(device), torch.cuda.stream(stream))
+        for g in self.guards:
+            g.__enter__()
+        return stream.cuda_stream
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+        return False
 
 
 def _workspace(nbytes, device, ws):
@@ -91,8 +110,8 @@ def _lin_args(q, k, v, log_decay, scale, lengths, S0):
         _need(lengths, "lengths", (B,), torch.int32, dev)
     if S0 is not None:
         _need(S0, "S0", (B, H, dk, dv), torch.float32, dev)
-    a = N.LinArgs(B=B, T=T, H=H, dk=dk, dv=dv, dtype=code, flags=0, scale=float(scale), q=_ptr(q), k=_ptr(k), v=_ptr(v),
-                  log_decay=_ptr(log_decay), lengths=_ptr(lengths), S0=_ptr(S0))
+    a = N.LinArgs(B, T, H, dk, dv, code, 0, float(scale), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                  _ptr(lengths), _ptr(S0))
     return a, (B, T, H, dk, dv, q.dtype, dev)
 
 
@@ -113,7 +132,7 @@ def lin_attn_fwd(q, k, v, log_decay, *, scale=1.0, lengths=None, S0=None, want_s
     no gradient."""
     a, (B, T, H, dk, dv, dt, dev) = _lin_args(q, k, v, log_decay, scale, lengths, S0)
     lib = N.load()
-    with _on(dev, stream) as s:
+    with _On(dev, stream) as s:
         y = _out(y, "y", (B, T, H, dv), dt, dev)
         S_T = _out(S_T, "S_T", (B, H, dk, dv), torch.float32, dev) if want_state else None
         nbytes = int(lib.muir_lin_fwd_workspace(C.byref(a)))
@@ -132,11 +151,11 @@ def lin_attn_bwd(q, k, v, log_decay, dy, *, scale=1.0, lengths=None, S0=None, dS
         _need(dS_T, "dS_T", (B, H, dk, dv), torch.float32, dev)
     lib = N.load()
     o = outputs or {}
-    with _on(dev, stream) as s:
+    with _On(dev, stream) as s:
         out = {"dq": _out(o.get("dq"), "dq", (B, T, H, dk), dt, dev), "dk": _out(o.get("dk"), "dk", (B, T, H, dk), dt, dev),
                "dv": _out(o.get("dv"), "dv", (B, T, H, dv), dt, dev),
                "dS0": _out(o.get("dS0"), "dS0", (B, H, dk, dv), torch.float32, dev) if want_dS0 else None}
-        g = N.LinGrads(dy=_ptr(dy), dS_T=_ptr(dS_T), **{n: _ptr(t) for n, t in out.items()})
+        g = N.LinGrads(dy.data_ptr(), _ptr(dS_T), *(_ptr(out[n]) for n in ("dq", "dk", "dv", "dS0")))
         nbytes = int(lib.muir_lin_bwd_workspace(C.byref(a)))
         ws = _workspace(nbytes, dev, workspace)
         N.check(lib.muir_lin_bwd(C.byref(a), C.byref(g), _ptr(ws), nbytes, s), "muir_lin_bwd")
@@ -154,10 +173,10 @@ def lin_attn_step(S, q, k, v, log_decay, *, scale=1.0, y=None, stream=None):
         _need(t, name, (n, H, d), q.dtype, dev)
     _need(log_decay, "log_decay", (H,), torch.float32, dev)
     lib = N.load()
-    with _on(dev, stream) as s:
+    with _On(dev, stream) as s:
         y = _out(y, "y", (n, H, dv), q.dtype, dev)
-        a = N.LinStepArgs(n_seq=n, H=H, dk=dk, dv=dv, dtype=code, scale=float(scale), S=_ptr(S), q=_ptr(q), k=_ptr(k),
-                          v=_ptr(v), log_decay=_ptr(log_decay), y=_ptr(y))
+        a = N.LinStepArgs(n, H, dk, dv, code, float(scale), S.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                          log_decay.data_ptr(), y.data_ptr())
         N.check(lib.muir_lin_step(C.byref(a), s), "muir_lin_step")
     return y
 
@@ -179,7 +198,7 @@ def rms_norm(x, weight, *, residual=None, eps=1e-6, y=None, h=None, rstd=None, s
     and, with a residual, h (the new residual stream; may be the residual's own buffer)."""
     n, d, dev, code = _norm_operands(x, weight, residual)
     lib = N.load()
-    with _on(dev, stream) as s:
+    with _On(dev, stream) as s:
         out = {"y": _out(y, "y", (n, d), x.dtype, dev), "rstd": _out(rstd, "rstd", (n,), torch.float32, dev)}
         if residual is not None:
             out["h"] = _out(h, "h", (n, d), x.dtype, dev)
@@ -193,7 +212,7 @@ def rms_norm_quant(x, weight, *, residual=None, eps=1e-6, q=None, scale=None, h=
     scale = max |y| / 448 of the row. Returns a dict of q, scale, rstd and, with a residual, h."""
     n, d, dev, code = _norm_operands(x, weight, residual)
     lib = N.load()
-    with _on(dev, stream) as s:
+    with _On(dev, stream) as s:
         out = {"q": _out(q, "q", (n, d), _E4M3, dev), "scale": _out(scale, "scale", (n,), torch.float32, dev),
                "rstd": _out(rstd, "rstd", (n,), torch.float32, dev)}
         if residual is not None:
@@ -217,7 +236,7 @@ def rms_norm_bwd(dy, h, weight, rstd, *, dh=None, dx=None, dweight=None, workspa
     if dh is not None:
         _need(dh, "dh", (n, d), h.dtype, dev)
     lib = N.load()
-    with _on(dev, stream) as s:
+    with _On(dev, stream) as s:
         dx = _out(dx, "dx", (n, d), h.dtype, dev)
         dweight = _out(dweight, "dweight", (d,), torch.float32, dev)
         nbytes = int(lib.muir_rms_norm_bwd_workspace(n, d))
@@ -237,7 +256,7 @@ def w4_quantize(w, *, group=128, stream=None):
     if group not in (32, 64, 128) or K % 128:
         raise ValueError(f"group must be 32, 64 or 128 and K a multiple of 128 (got {group}, {K})")
     lib = N.load()
-    with _on(dev, stream) as s:
+    with _On(dev, stream) as s:
         codes = torch.empty(O, K, dtype=torch.uint8, device=dev)
         scales = torch.empty(O, K // group, dtype=torch.bfloat16, device=dev)
         N.check(lib.muir_w4_quantize(_ptr(w), _ptr(codes), _ptr(scales), K, O, group, code, s), "muir_w4_quantize")
@@ -257,7 +276,7 @@ def w4_pack(codes, scales, *, stream=None):
     _need(scales, "scales", (O, ng), torch.bfloat16, dev)
     lib = N.load()
     tiles = (O + 15) // 16
-    with _on(dev, stream) as s:
+    with _On(dev, stream) as s:
         wq = torch.empty(tiles, K // 128, 1024, dtype=torch.uint8, device=dev)
         ws = torch.empty(tiles, K // 128, 128 // group, 16, dtype=torch.bfloat16, device=dev)
         N.check(lib.muir_w4_pack(_ptr(codes), _ptr(scales), _ptr(wq), _ptr(ws), K, O, group, s), "muir_w4_pack")
@@ -289,7 +308,7 @@ def w4_matvec(x, wq, ws, O, *, x_scale=None, out_dtype=None, y=None, stream=None
             raise ValueError("x_scale belongs to 8-bit rows")
         _need(x_scale, "x_scale", (n,), torch.float32, dev)
     lib = N.load()
-    with _on(dev, stream) as s:
+    with _On(dev, stream) as s:
         y = _out(y, "y", (n, O), ydt, dev)
         N.check(lib.muir_w4_matvec(_ptr(x), _ptr(x_scale), _ptr(wq), _ptr(ws), _ptr(y), n, K, O, 128 // gpb, code,
                                    N.MUIR_F32 if ydt == torch.float32 else N.MUIR_BF16, s), "muir_w4_matvec")
