@@ -20,31 +20,37 @@
 // and only its operand copy is rounded. So y has one bf16 rounding of each weight
 // and of the state, and the final state is fp32.
 //
-// Six products of 128 x 128 x 128 per chunk are 3072 tensor cycles of the about
-// 5700 that 128 KB of operands and output take at this GPU's copy bandwidth with
-// one CTA per SM: the pass is bound by memory when the tiles of the next chunk
-// arrive while this one computes. Shared memory decides that: 32 KB per tile, a
-// ring of five slots for a, b, c (the next chunk's a and b land during this
-// chunk, its c when this chunk's a has been used), one tile for S, and one for the
-// parts of b: the first part is written over b once the scores are done, the
-// second beside it, the third over the first: 224 KB.
+// A launch that keeps no final state (one of several segments: the final state comes
+// from the segments' own) feeds S only to y, at bf16 accuracy; there b is cut into
+// two parts, 17 bits, by three packed bf16 operations for two elements.
 //
-// Roles (768 threads): warp 0 issues TMA copies, warp 1 the MMAs; warps 4..7 (one
-// token row per thread) mask the scores and write outputs; warps 8..15 cut b (half
-// a token row per thread); warps 16..23 keep the state (one row, 64 columns per
-// thread). The products are issued y1(n), parts 1 and 2 (n), scores(n+1), part 3
-// (n), y2(n+1), so that the scores fill the wait for the third part and the
-// masking, cutting and outputs of one chunk run under the products of another.
-// The block is launched with 80 registers per thread; the warpgroups trade them
-// (64 + 96 + 2 x 64 + 2 x 96 = 6 x 80). Hand-offs are mbarriers with bounded
-// waits:
-//   full[s], empty[s]   slot s holds a tile / its last reader is done
+// Bound: per chunk 128 KB of operands and output, about 5700 cycles at this GPU's
+// copy bandwidth with one CTA per SM, against five products of 512 tensor cycles
+// (six with three parts) and about 3000 issue slots of each scheduler for the work
+// on elements. So the pass is bound by memory if the roles run side by side and the
+// next tiles are on their way, which is what the rest is for.
+//
+// Shared memory, 7 tiles of 32 KB: a ring of four for b, a, c (b first: it is cut
+// ahead of everything else and its slot is free again as soon as it has been cut and
+// multiplied), two for the parts, one for S. Third parts go over b itself. Without
+// outputs: the ring for b, c, first parts over b, two tiles for second parts (even
+// and odd chunks) and one for third parts, which are multiplied first.
+//
+// Roles (896 threads): warp 0 issues TMA copies, warp 1 the MMAs; warps 4..11 mask
+// the scores (one token row, 64 columns per thread); warps 12..19 cut b (half a
+// token row per thread); warps 20..27 keep the state and write outputs (one row, 64
+// columns per thread). The products are issued parts(n), y2(n), y1(n), scores(n+1):
+// the parts and y2 run while the scores are masked. The block is launched with 72
+// registers per thread; the warpgroups trade them (40 + 2 x 56 + 2 x 64 + 2 x 112 =
+// 7 x 72). Hand-offs are mbarriers with bounded waits:
+//   full[s], empty[s]   slot s holds a tile / its readers are done (one commit and
+//                       the eight cutting warps)
 //   scores    scores in TMEM               (MMA -> mask, cut)
 //   weights   masked scores in TMEM        (mask -> MMA)
-//   y         y1 and y2 in TMEM            (MMA -> mask)
-//   y_free    y1 and y2 read               (mask -> MMA)
-//   cut12, cut3   parts 1 and 2 / 3 of b in shared memory (cut -> MMA)
-//   used12    parts 1 and 2 used           (MMA -> cut)
+//   y2, y     y2 / y1 and y2 in TMEM       (MMA -> state)
+//   y_free    y1 and y2 read               (state -> MMA)
+//   cut       the parts in shared memory   (cut -> MMA)
+//   used3     third parts used             (MMA -> cut; without outputs)
 //   ds        dS in TMEM                   (MMA -> state, cut)
 //   ds_free   dS read                      (state -> MMA)
 //   s_ready   S for the next chunk in shared memory (state -> MMA)
@@ -56,9 +62,9 @@
 namespace muir {
 
 constexpr int kLtChunk = 128;
-constexpr int kLtThreads = 768;
+constexpr int kLtThreads = 896;
 constexpr uint32_t kLtTile = 32768, kLtBox = 16384;  // 128 rows x 128 columns bf16: two boxes of 64 columns
-constexpr int kLtSlots = 5;
+constexpr int kLtSlots = 4;
 constexpr uint32_t kLtSmem = 7 * kLtTile + 1024;
 
 constexpr int kLinMaxPasses = 3;
@@ -91,37 +97,45 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
 // not be slower than the tensor core (64 cycles for 128 x 128 x 16): with unrolled
 // steps, constant offsets added to one descriptor and constant flags a step takes
 // 65 cycles; with flags and step counts from registers it took 180 to 270.
+// A descriptor is its low word; the high one (stride of 8-row groups 1024 bytes,
+// version, 128-byte swizzle) is the same for every tile here.
+constexpr uint32_t kLtDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t lt_desc(uint32_t saddr, uint32_t lbo) { return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16); }
+
 template <bool ACC>
-__device__ __forceinline__ void mma_step(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc) {
+__device__ __forceinline__ void mma_step(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0)
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 x, {%1, %4};\n\t"
+      "mov.b64 y, {%2, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a), "r"(b), "r"(idesc), "n"(kLtDescHi), "n"(ACC ? 1 : 0)
       : "memory");
 }
 // The same with the A operand in TMEM (row = lane, two bf16 per column).
 template <bool ACC>
-__device__ __forceinline__ void mma_step_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc) {
+__device__ __forceinline__ void mma_step_ta(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "n"(ACC ? 1 : 0)
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 y, {%2, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b), "r"(idesc), "n"(kLtDescHi), "n"(ACC ? 1 : 0)
       : "memory");
 }
 
 // Step j of 16 channels of a K-major tile / of 16 rows of an MN-major one, in
 // descriptor units of 16 bytes.
-__host__ __device__ constexpr uint64_t lt_kstep(int j) { return (uint64_t)(((j >> 2) * kLtBox + (j & 3) * 32u) >> 4); }
-__host__ __device__ constexpr uint64_t lt_mnstep(int j) { return (uint64_t)((j * 2048u) >> 4); }
+__host__ __device__ constexpr uint32_t lt_kstep(int j) { return ((j >> 2) * kLtBox + (j & 3) * 32u) >> 4; }
+__host__ __device__ constexpr uint32_t lt_mnstep(int j) { return (j * 2048u) >> 4; }
 
 template <int STEPS, bool ACC, bool A_MN, bool B_MN>
 __device__ __forceinline__ void lt_product(uint32_t d_tmem, uint32_t at, uint32_t bt, uint32_t idesc) {
-  const uint64_t a = sdesc_sw128(at, A_MN ? kLtBox : 16u, 1024u), b = sdesc_sw128(bt, B_MN ? kLtBox : 16u, 1024u);
+  const uint32_t a = lt_desc(at, A_MN ? kLtBox : 16u), b = lt_desc(bt, B_MN ? kLtBox : 16u);
 #pragma unroll
   for (int j = 0; j < STEPS; ++j) {
-    const uint64_t aj = a + (A_MN ? lt_mnstep(j) : lt_kstep(j)), bj = b + (B_MN ? lt_mnstep(j) : lt_kstep(j));
+    const uint32_t aj = a + (A_MN ? lt_mnstep(j) : lt_kstep(j)), bj = b + (B_MN ? lt_mnstep(j) : lt_kstep(j));
     if (ACC || j > 0) mma_step<true>(d_tmem, aj, bj, idesc);
     else mma_step<false>(d_tmem, aj, bj, idesc);
   }
@@ -144,17 +158,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
-// 32 columns from each of two places of this thread's lane: both loads, one wait.
-__device__ __forceinline__ void tmem_ld32x2(uint32_t ta, uint32_t tb, float (&a)[32], float (&b)[32]) {
-  uint32_t r[32], s[32];
-  auto issue = [](uint32_t t, uint32_t (&x)[32]) {
+// 16 columns from each of two places of this thread's lane: both loads, one wait.
+__device__ __forceinline__ void tmem_ld16x2(uint32_t ta, uint32_t tb, float (&a)[16], float (&b)[16]) {
+  uint32_t r[16], s[16];
+  auto issue = [](uint32_t t, uint32_t (&x)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]), "=r"(x[8]),
-          "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15]), "=r"(x[16]), "=r"(x[17]),
-          "=r"(x[18]), "=r"(x[19]), "=r"(x[20]), "=r"(x[21]), "=r"(x[22]), "=r"(x[23]), "=r"(x[24]), "=r"(x[25]), "=r"(x[26]),
-          "=r"(x[27]), "=r"(x[28]), "=r"(x[29]), "=r"(x[30]), "=r"(x[31])
+          "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15])
         : "r"(t)
         : "memory");
   };
@@ -162,7 +173,7 @@ __device__ __forceinline__ void tmem_ld32x2(uint32_t ta, uint32_t tb, float (&a)
   issue(tb, s);
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {  // after the wait: the registers are not valid before it
+  for (int i = 0; i < 16; ++i) {  // uses come after the wait: the registers are not valid before it
     asm volatile("" : "+r"(r[i]), "+r"(s[i]));
     a[i] = __uint_as_float(r[i]);
     b[i] = __uint_as_float(s[i]);
@@ -222,7 +233,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
   extern __shared__ __align__(1024) uint8_t lt_sm[];
   constexpr int SLOTS = kLtSlots;
   constexpr int TILES = OUT ? 3 : 2;  // per chunk: a, b, c or b, c
-  __shared__ uint64_t full[SLOTS], empty[SLOTS], b_scores, b_weights, b_y2, b_y, b_yfree, b_cut12, b_cut3, b_used12, b_ds, b_dsfree, b_sready;
+  __shared__ uint64_t full[SLOTS], empty[SLOTS], b_scores, b_weights, b_y2, b_y, b_yfree, b_cut, b_used3, b_ds, b_dsfree, b_sready;
   __shared__ uint32_t tslot;
   __shared__ float pw[kLtChunk];              // lambda^0 ..
   __shared__ __align__(16) float pcol[32];    // column factors inside a block of 32 (see the mask)
@@ -231,22 +242,23 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const LinUnit u = lin_unit(p);
   const uint32_t base = (smem_u32(lt_sm) + 1023u) & ~1023u;
-  // beside the ring: the second parts' tile, and S's or (without outputs) a second one
-  const uint32_t x_tile = base + 5u * kLtTile, s_tile = base + 6u * kLtTile;
-  auto x_of = [&](int n) { return OUT ? x_tile : x_tile + (uint32_t)(n & 1) * kLtTile; };
+  // the parts of chunk n's b, given b's own tile
+  const uint32_t spare = base + (uint32_t)SLOTS * kLtTile, s_tile = spare + 2u * kLtTile;
+  auto part1 = [&](int n, uint32_t bt) { return OUT ? spare : bt; };
+  auto part2 = [&](int n, uint32_t bt) { return spare + (OUT ? 1u : (uint32_t)(n & 1)) * kLtTile; };
+  auto part3 = [&](int n, uint32_t bt) { return OUT ? bt : spare + 2u * kLtTile; };
   if (tid == 0) {
     for (int i = 0; i < SLOTS; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], 9);
     }
     mbar_init(&b_scores, 1);
-    mbar_init(&b_weights, 4);
+    mbar_init(&b_weights, 8);
     mbar_init(&b_y2, 1);
     mbar_init(&b_y, 1);
-    mbar_init(&b_yfree, 4);
-    mbar_init(&b_cut12, 8);
-    mbar_init(&b_cut3, 8);
-    mbar_init(&b_used12, 1);
+    mbar_init(&b_yfree, 8);
+    mbar_init(&b_cut, 8);
+    mbar_init(&b_used3, 1);
     mbar_init(&b_ds, 1);
     mbar_init(&b_dsfree, 8);
     mbar_init(&b_sready, 8);
@@ -263,23 +275,22 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
   auto chunk_at = [&](int n) { return p.reverse ? u.chunks - 1 - n : n; };
 
   if (warp < 4) {
-    regs_dec<64>();
+    regs_dec<40>();
     if (warp == 0) {
-    // ---- TMA: tiles in the order they are needed, a(n) b(n) c(n) a(n+1) .. --------
+    // ---- TMA: tiles in the order they are needed, b(n) a(n) c(n) b(n+1) .. --------
     if (lane == 0) {
-      const int abytes = p.da > 64 ? 32768 : 16384, cbytes = p.dc > 64 ? 32768 : 16384;
       bool ok = true;
       int m = 0;
       for (int n = 0; n < u.chunks && ok; ++n) {
         const int t = (int)(u.t0 + (int64_t)chunk_at(n) * kLtChunk);
-        for (int k = OUT ? 0 : 1; k < 3 && ok; ++k, ++m) {
+        for (int k = 0; k < TILES && ok; ++k, ++m) {
           const int s = m % SLOTS, turn = m / SLOTS;
           if (turn > 0) ok = mbar_wait(&empty[s], (uint32_t)(turn - 1) & 1u);
           if (!ok) break;
-          const CUtensorMap* map = k == 0 ? &args.a[pi] : k == 1 ? &args.b[pi] : &args.c[pi];
-          const int d = k == 2 ? p.dc : p.da;
+          const CUtensorMap* map = k == 0 ? &args.b[pi] : k == TILES - 1 ? &args.c[pi] : &args.a[pi];
+          const int d = k == TILES - 1 ? p.dc : p.da;
           const uint32_t dst = base + (uint32_t)s * kLtTile;
-          mbar_expect_tx(&full[s], (uint32_t)(k == 2 ? cbytes : abytes));
+          mbar_expect_tx(&full[s], d > 64 ? 2u * kLtBox : kLtBox);
           tma_load_3d(dst, map, u.h * d, t, u.b, &full[s]);
           if (d > 64) tma_load_3d(dst + kLtBox, map, u.h * d + 64, t, u.b, &full[s]);
         }
@@ -308,8 +319,9 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       if (!landed(m) || !landed(m + 1) || (n > 0 && !warp_wait(&b_y, (uint32_t)(n - 1) & 1u))) return false;
       tc_fence_after();
       if (leader) {
-        lt_product_k<false>(p.da, m_scores, slot(m), slot(m + 1), id_scores);
+        lt_product_k<false>(p.da, m_scores, slot(m + 1), slot(m), id_scores);
         mma_commit(&b_scores);
+        if (PARTS == 2) mma_commit(&empty[m % SLOTS]);
       }
       __syncwarp();
       return true;
@@ -317,16 +329,24 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
     if (OUT && chunks > 0) ok = scores(0);
     for (int n = 0; n < chunks && ok; ++n) {
       const uint32_t ph = (uint32_t)n & 1u;
-      const int ma = n * TILES, mb = ma + TILES - 2, mc = ma + TILES - 1;
-      const uint32_t at = slot(ma), bt = slot(mb), ct = slot(mc);
+      const int mb = n * TILES, ma = mb + 1, mc = mb + TILES - 1;
+      const uint32_t bt = slot(mb), ct = slot(mc);
       // c's tile: landed, and its rows past the last token cleared by the cutters
-      ok = landed(mc) && warp_wait(&b_cut12, ph) && (n == 0 || warp_wait(&b_dsfree, ph ^ 1u));
+      ok = landed(mc) && warp_wait(&b_cut, ph) && (n == 0 || warp_wait(&b_dsfree, ph ^ 1u));
       if (!ok) break;
       tc_fence_after();
       if (leader) {
-        lt_product<8, false, true, true>(m_ds, bt, ct, id_ds);
-        lt_product<8, true, true, true>(m_ds, x_of(n), ct, id_ds);
-        mma_commit(PARTS == 2 ? &b_ds : &b_used12);
+        if (PARTS == 3) {
+          lt_product<8, false, true, true>(m_ds, part3(n, bt), ct, id_ds);
+          if (!OUT) mma_commit(&b_used3);
+          lt_product<8, true, true, true>(m_ds, part2(n, bt), ct, id_ds);
+        } else {
+          lt_product<8, false, true, true>(m_ds, part2(n, bt), ct, id_ds);
+        }
+        lt_product<8, true, true, true>(m_ds, part1(n, bt), ct, id_ds);
+        mma_commit(&b_ds);
+        if (PARTS == 3) mma_commit(&empty[mb % SLOTS]);
+        if (!OUT) mma_commit(&empty[mc % SLOTS]);
       }
       __syncwarp();
       if (OUT) {
@@ -334,7 +354,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
         if (!ok) break;
         tc_fence_after();
         if (leader) {
-          lt_product_k<true>(p.da, m_y2, at, s_tile, id_y);
+          lt_product_k<true>(p.da, m_y2, slot(ma), s_tile, id_y);
           mma_commit(&b_y2);
           mma_commit(&empty[ma % SLOTS]);
         }
@@ -343,30 +363,16 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
         if (!ok) break;
         tc_fence_after();
         if (leader) {
-          const uint64_t cd = sdesc_sw128(ct, kLtBox, 1024u);
+          const uint32_t cd = lt_desc(ct, kLtBox);
           mma_step_ta<false>(m_y1, m_scores, cd, id_y);
 #pragma unroll
-          for (int j = 1; j < 8; ++j) mma_step_ta<true>(m_y1, m_scores + (uint32_t)j * 8u, cd + lt_mnstep(j), id_y);
+          for (int j = 1; j < 8; ++j)
+            mma_step_ta<true>(m_y1, m_scores + (uint32_t)(j < 4 ? 8 * j : 32 + 8 * j), cd + lt_mnstep(j), id_y);
           mma_commit(&b_y);
-          if (PARTS == 2) {
-            mma_commit(&empty[mb % SLOTS]);
-            mma_commit(&empty[mc % SLOTS]);
-          }
-        }
-        __syncwarp();
-        if (n + 1 < chunks) ok = scores(n + 1);
-      }
-      if (PARTS == 3) {
-        ok = ok && warp_wait(&b_cut3, ph);
-        if (!ok) break;
-        tc_fence_after();
-        if (leader) {
-          lt_product<8, true, true, true>(m_ds, bt, ct, id_ds);
-          mma_commit(&b_ds);
-          mma_commit(&empty[mb % SLOTS]);
           mma_commit(&empty[mc % SLOTS]);
         }
         __syncwarp();
+        if (n + 1 < chunks) ok = scores(n + 1);
       }
     }
     // every issued product has completed when the CTA ends: the last chunk's commits
@@ -383,22 +389,16 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       mbar_wait_for(&b_ds, 1u, 1000000ull);
     }
     }
-  } else if (warp < 8) {
-    // ---- mask and outputs: thread = token row i of the chunk ----------------------------
-    regs_inc<96>();
+  } else if (warp < 12) {
+    // ---- mask: thread = token row i of the chunk, 64 of its columns -------------------------
+    regs_dec<56>();
     if constexpr (OUT) {
-    const int w = warp & 3, i = w * 32 + lane;
+    const int w = warp & 3, i = w * 32 + lane, k0 = warp < 8 ? 0 : 2;
     const uint32_t row = tmem_lane_base(warp);
-    __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(p.out) + (((int64_t)u.b * p.T + u.t0) * p.H + u.h) * p.dc;
-    const int64_t pitch = (int64_t)p.H * p.dc;
-    {  // padded tokens of this segment: zeros
-      const int64_t end = (u.t0 + p.seglen < p.T ? p.seglen : p.T - u.t0);
-      const int pieces = p.dc / 8;
-      for (int64_t x = u.valid * pieces + i; x < end * pieces; x += 128)
-        *reinterpret_cast<uint4*>(out + (x / pieces) * pitch + (x % pieces) * 8) = make_uint4(0u, 0u, 0u, 0u);
-    }
     // lambda^gap = (row factor of a block of 32 columns) (column factor in the block),
-    // both at most 1 for blocks off the diagonal
+    // both at most 1 for blocks off the diagonal; on it the row factor is up to
+    // lambda^-31, which decays above 2^-3.75 keep below 2^117
+    const bool mild = u.c2 > -3.75f;
     bool ok = true;
     for (int n = 0; n < u.chunks && ok; ++n) {
       const uint32_t ph = (uint32_t)n & 1u;
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       if (!ok) break;
       tc_fence_after();
 #pragma unroll 1
-      for (int k = 0; k < 4; ++k) {
+      for (int k = k0; k < k0 + 2; ++k) {
         uint32_t wd[16];
         const bool none = p.reverse ? k < w : k > w;
         if (none) {  // whole warp: masked block
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
         } else {
           float v[32];
           tmem_ld32(t_scores + row + (uint32_t)(32 * k), v);
-          if (k == w) {
+          if (k == w && !mild) {
             const int last = L - 32 * k;  // columns from here on are past the last token
 #pragma unroll
             for (int s = 0; s < 32; ++s) {
@@ -429,8 +429,14 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
 #pragma unroll
             for (int q = 0; q < 16; ++q) wd[q] = bf16x2(v[2 * q], v[2 * q + 1]);
           } else {
-            const float rf = p.p_scale * pw[p.reverse ? 32 * k - i : i - 32 * k - 31];
+            // on the diagonal the row factor's exponent is 0 .. -31 (mild decays only)
+            const float rf = p.p_scale * (k == w ? exp2f(u.c2 * (float)(p.reverse ? -lane : lane - 31))
+                                                 : pw[p.reverse ? 32 * k - i : i - 32 * k - 31]);
             const float2 rf2 = make_float2(rf, rf);
+            if (k == w) {
+#pragma unroll
+              for (int s = 0; s < 32; ++s) v[s] = (p.reverse ? s >= lane : s <= lane) ? v[s] : 0.f;
+            }
             if (32 * k + 32 > L) {  // columns past the last token
 #pragma unroll
               for (int s = 0; s < 32; ++s) v[s] = 32 * k + s < L ? v[s] : 0.f;
@@ -445,133 +451,92 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
             }
           }
         }
-        // columns 16 k .. of the scores have been read: block k's weights go there
-        tmem_st16(t_scores + row + (uint32_t)(16 * k), wd);
+        // over scores that this thread has read: blocks 0, 1 to columns 0 .. 31, 2, 3 to 64 .. 95
+        tmem_st16(t_scores + row + (uint32_t)(16 * k + (k < 2 ? 0 : 32)), wd);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive1(&b_weights);
-      ok = warp_wait(&b_y, ph);
-      if (!ok) break;
-      tc_fence_after();
-      const float rw = p.o_scale * (p.reverse ? pw[i < L ? L - 1 - i : 0] : exp2f(u.c2 * (float)(i + 1)));
-#pragma unroll 1
-      for (int c = 0; c < p.dc; c += 32) {
-        float y1[32], y2[32];
-        tmem_ld32x2(t_y1 + row + (uint32_t)c, t_y2 + row + (uint32_t)c, y1, y2);
-        if (c + 32 >= p.dc) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive1(&b_yfree);
-        }
-        if (i < L) {
-          __nv_bfloat16* d = out + (r0 + i) * pitch + c;
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            uint32_t o[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const int e = 16 * hf + 2 * q;
-              const float2 y = __ffma2_rn(make_float2(rw, rw), make_float2(y2[e], y2[e + 1]), make_float2(y1[e], y1[e + 1]));
-              o[q] = bf16x2(y.x, y.y);
-            }
-            stg_bf16x16(d + 16 * hf, o);
-          }
-        }
-      }
     }
     }
-  } else if (warp < 16) {
+  } else if (warp < 20) {
     // ---- cut b: thread = half a token row ---------------------------------------------------
     regs_dec<64>();
-    const int half = (warp - 8) >> 2;      // columns 64 half ..
+    const int half = (warp - 12) >> 2;     // columns 64 half ..
     const int r = (warp & 3) * 32 + lane;  // token row
     const int bcols = p.da - 64 * half < 64 ? p.da - 64 * half : 64;  // at most 0: none
     const uint32_t place = (uint32_t)half * kLtBox + (uint32_t)r * 128u;
     bool ok = true;
     for (int n = 0; n < u.chunks && ok; ++n) {
-      const uint32_t ph = (uint32_t)n & 1u;
       const int64_t r0 = (int64_t)chunk_at(n) * kLtChunk;
       const int L = (int)(u.valid - r0 < kLtChunk ? u.valid - r0 : kLtChunk);
-      const int m = n * TILES + TILES - 2;
-      const int sb = m % SLOTS, sc = (m + 1) % SLOTS;
-      const uint32_t line = base + (uint32_t)sb * kLtTile + place;
-      const uint32_t xline = x_of(n) + place;
+      const int mb = n * TILES, mc = mb + TILES - 1;
+      const uint32_t bt = base + (uint32_t)(mb % SLOTS) * kLtTile;
+      const uint32_t line = bt + place, l1 = part1(n, bt) + place, l2 = part2(n, bt) + place, l3 = part3(n, bt) + place;
       const float wt = r < L ? p.u_scale * exp2f(u.c2 * (float)(p.reverse ? r + 1 : L - 1 - r)) : 0.f;
-      ok = warp_wait(&full[sb], (uint32_t)(m / SLOTS) & 1u) && warp_wait(&full[sc], (uint32_t)((m + 1) / SLOTS) & 1u);
-      if (OUT) {
-        ok = ok && warp_wait(&b_scores, ph);  // b itself has been used, and the last second parts
-        if (PARTS == 2 && n > 0) ok = ok && warp_wait(&b_ds, ph ^ 1u);
-      }
+      ok = warp_wait(&full[mb % SLOTS], (uint32_t)(mb / SLOTS) & 1u);
+      if (L < kLtChunk) ok = ok && warp_wait(&full[mc % SLOTS], (uint32_t)(mc / SLOTS) & 1u);
+      // the tiles of the last parts have been used; before third parts go over b, the scores have been formed
+      if (n > 0) ok = ok && warp_wait(OUT ? &b_ds : &b_used3, (uint32_t)(n - 1) & 1u);
+      if (OUT && PARTS == 3) ok = ok && warp_wait(&b_scores, (uint32_t)n & 1u);
       if (!ok) break;
-      uint32_t x[32];  // the half row, then its third parts
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const uint4 v = *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(line + (uint32_t)((c ^ (r & 7)) << 4)));
-        x[4 * c] = v.x;
-        x[4 * c + 1] = v.y;
-        x[4 * c + 2] = v.z;
-        x[4 * c + 3] = v.w;
-      }
-      if (r >= L) {  // rows past the last token count as zeros, whatever they hold
-#pragma unroll
-        for (int c = 0; c < 32; ++c) x[c] = 0u;
-      }
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        uint32_t p1[4], p2[4];
-        const float2 minus = make_float2(-1.f, -1.f);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t in = x[4 * c + q];
-          float2 f = __fmul2_rn(make_float2(__uint_as_float(in << 16), __uint_as_float(in & 0xFFFF0000u)), make_float2(wt, wt));
-          if (PARTS == 2) {
-            p1[q] = bf16x2(f.x, f.y);
-            f = __ffma2_rn(make_float2(__uint_as_float(p1[q] << 16), __uint_as_float(p1[q] & 0xFFFF0000u)), minus, f);
-            p2[q] = bf16x2(f.x, f.y);
-          } else {
-            auto upper = [&]() {
-              return make_float2(__uint_as_float(__float_as_uint(f.x) & 0xFFFF0000u),
-                                 __uint_as_float(__float_as_uint(f.y) & 0xFFFF0000u));
-            };
-            auto pack = [&]() { return __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632); };
-            p1[q] = pack();
-            f = __ffma2_rn(upper(), minus, f);
-            p2[q] = pack();
-            f = __ffma2_rn(upper(), minus, f);
-            x[4 * c + q] = pack();
-          }
-        }
-        if (8 * c < bcols) {
+      // packed bf16, two parts: with the weight as w1 + w2, p1 = b w1 rounded, and
+      // p2 = (b w1 - p1) + b w2, the bracket exact, rounded once
+      const __nv_bfloat16 w1 = __float2bfloat16_rn(wt), w2 = __float2bfloat16_rn(wt - __bfloat162float(w1));
+      const __nv_bfloat162 w11 = __halves2bfloat162(w1, w1), w22 = __halves2bfloat162(w2, w2);
+      if (bcols > 0) {
+#pragma unroll 4
+        for (int c = 0; c < 8; ++c) {
           const uint32_t at = (uint32_t)((c ^ (r & 7)) << 4);
-          sts128(line + at, make_uint4(p1[0], p1[1], p1[2], p1[3]));
-          sts128(xline + at, make_uint4(p2[0], p2[1], p2[2], p2[3]));
+          uint4 v = *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(line + at));
+          if (r >= L) v = make_uint4(0u, 0u, 0u, 0u);  // past the last token: zeros, whatever they hold
+          const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+          uint32_t p1[4], p2[4], p3[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if constexpr (PARTS == 3) {  // the upper 16 bits of the fp32 product, of its rest, of the rest of that
+              float2 f = __fmul2_rn(make_float2(__uint_as_float(in[q] << 16), __uint_as_float(in[q] & 0xFFFF0000u)),
+                                    make_float2(wt, wt));
+              auto rest = [&]() {
+                const uint32_t hi = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
+                f = __ffma2_rn(make_float2(__uint_as_float(__float_as_uint(f.x) & 0xFFFF0000u),
+                                           __uint_as_float(__float_as_uint(f.y) & 0xFFFF0000u)),
+                               make_float2(-1.f, -1.f), f);
+                return hi;
+              };
+              p1[q] = rest();
+              p2[q] = rest();
+              p3[q] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
+            } else {
+              const __nv_bfloat162 bb = *reinterpret_cast<const __nv_bfloat162*>(&in[q]);
+              const __nv_bfloat162 h = __hmul2(bb, w11);
+              const __nv_bfloat162 l = __hfma2(bb, w22, __hfma2(bb, w11, __hneg2(h)));
+              p1[q] = *reinterpret_cast<const uint32_t*>(&h);
+              p2[q] = *reinterpret_cast<const uint32_t*>(&l);
+            }
+          }
+          // (columns past da hold other heads' channels: cut as well, rows of dS that nobody reads)
+          sts128(l1 + at, make_uint4(p1[0], p1[1], p1[2], p1[3]));
+          sts128(l2 + at, make_uint4(p2[0], p2[1], p2[2], p2[3]));
+          if (PARTS == 3) sts128(l3 + at, make_uint4(p3[0], p3[1], p3[2], p3[3]));
         }
       }
       if (r >= L) {  // c's rows past the last token: zero times anything must stay zero
-        const uint32_t cline = base + (uint32_t)sc * kLtTile + place;
+        const uint32_t cline = base + (uint32_t)(mc % SLOTS) * kLtTile + place;
 #pragma unroll
         for (int c = 0; c < 8; ++c) sts128(cline + (uint32_t)(c << 4), make_uint4(0u, 0u, 0u, 0u));
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive1(&b_cut12);
-      if (PARTS == 3) {
-        ok = warp_wait(&b_used12, ph);
-        if (!ok) break;
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          if (8 * c < bcols)
-            sts128(line + (uint32_t)((c ^ (r & 7)) << 4), make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]));
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive1(&b_cut3);
+      if (lane == 0) {
+        mbar_arrive1(&b_cut);
+        for (int m = mb; m <= mc; ++m) mbar_arrive1(&empty[m % SLOTS]);
       }
     }
   } else {
-    // ---- the state: thread = row r, columns 64 half .. -----------------------------------------
-    regs_inc<96>();
-    const int half = (warp - 16) >> 2;
+    // ---- the state and outputs: thread = row r, columns 64 half .. ---------------------------------
+    regs_inc<112>();
+    const int half = (warp - 20) >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t row = tmem_lane_base(warp);
     const int nstate = p.da * p.dc;
@@ -609,6 +574,41 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       if (lane == 0) mbar_arrive1(&b_sready);
     };
     if constexpr (OUT) put_state();
+    __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(p.out) + (((int64_t)u.b * p.T + u.t0) * p.H + u.h) * p.dc;
+    const int64_t pitch = (int64_t)p.H * p.dc;
+    if constexpr (OUT) {  // padded tokens of this segment: zeros
+      const int64_t end = (u.t0 + p.seglen < p.T ? p.seglen : p.T - u.t0);
+      const int pieces = p.dc / 8;
+      for (int64_t x = u.valid * pieces + tid - 640; x < end * pieces; x += 256)
+        *reinterpret_cast<uint4*>(out + (x / pieces) * pitch + (x % pieces) * 8) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    // outputs of chunk n: row r, columns 64 half ..
+    auto outputs = [&](int n) {
+      const int64_t r0 = (int64_t)chunk_at(n) * kLtChunk;
+      const int L = (int)(u.valid - r0 < kLtChunk ? u.valid - r0 : kLtChunk);
+      if (!warp_wait(&b_y, (uint32_t)n & 1u)) return false;
+      tc_fence_after();
+      const float rw = p.o_scale * (p.reverse ? pw[r < L ? L - 1 - r : 0] : exp2f(u.c2 * (float)(r + 1)));
+      const float2 rw2 = make_float2(rw, rw);
+#pragma unroll 1
+      for (int c = 64 * half; c < 64 * half + 64 && c < p.dc; c += 16) {
+        float y1[16], y2[16];
+        tmem_ld16x2(t_y1 + row + (uint32_t)c, t_y2 + row + (uint32_t)c, y1, y2);
+        if (r < L) {
+          uint32_t o[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float2 y = __ffma2_rn(rw2, make_float2(y2[2 * q], y2[2 * q + 1]), make_float2(y1[2 * q], y1[2 * q + 1]));
+            o[q] = bf16x2(y.x, y.y);
+          }
+          stg_bf16x16(out + (r0 + r) * pitch + c, o);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive1(&b_yfree);
+      return true;
+    };
     bool ok = true;
     for (int n = 0; n < u.chunks && ok; ++n) {
       const int64_t r0 = (int64_t)chunk_at(n) * kLtChunk;
@@ -618,14 +618,14 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        if (64 * half + 32 * q < p.dc) {  // whole warps
-          float d[32];
-          tmem_ld32(t_ds + row + (uint32_t)(64 * half + 32 * q), d);
+      for (int q = 0; q < 4; ++q) {
+        if (64 * half + 16 * q < p.dc) {  // whole warps
+          float d[16];
+          tmem_ld16(t_ds + row + (uint32_t)(64 * half + 16 * q), d);
           const float2 g = make_float2(wl.g, wl.g), e = make_float2(wl.e, wl.e);
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            float* s2 = S + 32 * q + j;
+          for (int j = 0; j < 16; j += 2) {
+            float* s2 = S + 16 * q + j;
             const float2 old = make_float2(s2[0], s2[1]);
             const float2 now = __ffma2_rn(g, old, __ffma2_rn(e, old, make_float2(d[j], d[j + 1])));
             s2[0] = now.x;
@@ -641,6 +641,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
         if (!ok) break;
         put_state();
       }
+      if (OUT) ok = outputs(n);
     }
     float* dst = nullptr;
     if constexpr (!OUT) dst = p.seg + ((int64_t)u.bh * p.nseg + u.seg) * nstate;
