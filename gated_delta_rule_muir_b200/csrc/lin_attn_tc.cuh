@@ -148,13 +148,12 @@ __device__ __forceinline__ void lt_product_k(int channels, uint32_t d_tmem, uint
   else lt_product<2, false, false, B_MN>(d_tmem, at, bt, idesc);
 }
 
-// 16 columns (32-bit words) of this thread's lane; completes before return.
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+// 8 columns (32-bit words) of this thread's lane; completes before return.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};\n\t"
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};\n\t"
       "tcgen05.wait::st.sync.aligned;" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
       : "memory");
 }
 
@@ -236,7 +235,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
   __shared__ uint64_t full[SLOTS], empty[SLOTS], b_scores, b_weights, b_y2, b_y, b_yfree, b_cut, b_used3, b_ds, b_dsfree, b_sready;
   __shared__ uint32_t tslot;
   __shared__ float pw[kLtChunk];              // lambda^0 ..
-  __shared__ __align__(16) float pcol[32];    // column factors inside a block of 32 (see the mask)
+  __shared__ __align__(16) float pcol[16];    // column factors of 16 columns (see the mask)
   const int pi = blockIdx.y;
   const LinPass p = args.p[pi];  // by value: the waits between uses would reload what a reference names
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -265,7 +264,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
   }
   if (warp == 0) tmem_alloc(&tslot, 512);
   if (tid < kLtChunk) pw[tid] = exp2f(u.c2 * (float)tid);
-  if (tid < 32) pcol[tid] = exp2f(u.c2 * (float)(p.reverse ? tid : 31 - tid));
+  if (tid < 16) pcol[tid] = exp2f(u.c2 * (float)(p.reverse ? tid : 15 - tid));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -393,12 +392,13 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
     // ---- mask: thread = token row i of the chunk, 64 of its columns -------------------------
     regs_dec<56>();
     if constexpr (OUT) {
-    const int w = warp & 3, i = w * 32 + lane, k0 = warp < 8 ? 0 : 2;
+    const int w = warp & 3, i = w * 32 + lane, c0 = warp < 8 ? 0 : 64;
     const uint32_t row = tmem_lane_base(warp);
-    // lambda^gap = (row factor of a block of 32 columns) (column factor in the block),
-    // both at most 1 for blocks off the diagonal; on it the row factor is up to
-    // lambda^-31, which decays above 2^-3.75 keep below 2^117
-    const bool mild = u.c2 > -3.75f;
+    // 16 columns at a time in one short loop (an unrolled body of this size runs at the
+    // pace of instruction fetches). lambda^gap = (row factor) (column factor), the
+    // column factor at most 1 and the row factor at most lambda^-15: below 2^-8 that
+    // could overflow, and the powers are formed one by one.
+    const bool mild = u.c2 > -8.f;
     bool ok = true;
     for (int n = 0; n < u.chunks && ok; ++n) {
       const uint32_t ph = (uint32_t)n & 1u;
@@ -408,51 +408,44 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       if (!ok) break;
       tc_fence_after();
 #pragma unroll 1
-      for (int k = k0; k < k0 + 2; ++k) {
-        uint32_t wd[16];
-        const bool none = p.reverse ? k < w : k > w;
-        if (none) {  // whole warp: masked block
+      for (int c = c0; c < c0 + 64; c += 16) {
+        // columns lo .. hi - 1 of the 16 count
+        const int lo = p.reverse ? i - c : 0, hi = (p.reverse ? L : (i + 1 < L ? i + 1 : L)) - c;
+        uint32_t wd[8];
+        if (p.reverse ? c + 15 < 32 * w : c > 32 * w + 31) {  // none of any row of the warp
 #pragma unroll
-          for (int q = 0; q < 16; ++q) wd[q] = 0u;
+          for (int q = 0; q < 8; ++q) wd[q] = 0u;
         } else {
-          float v[32];
-          tmem_ld32(t_scores + row + (uint32_t)(32 * k), v);
-          if (k == w && !mild) {
-            const int last = L - 32 * k;  // columns from here on are past the last token
+          float v[16];
+          tmem_ld16(t_scores + row + (uint32_t)c, v);
+          const int e = p.reverse ? c - i : i - c - 15;
+          if (__any_sync(0xffffffffu, lo > 0 || hi < 16)) {
+            // dropped, not multiplied by zero: a score that does not count may be anything
 #pragma unroll
-            for (int s = 0; s < 32; ++s) {
-              const int gap = p.reverse ? s - lane : lane - s;
-              const float f = v[s] * (p.p_scale * pw[gap & 31]);
-              // dropped, not multiplied by zero: a masked score may be anything
-              v[s] = (gap >= 0) & (s < last) ? f : 0.f;
+            for (int s = 0; s < 16; ++s) v[s] = (s >= lo) & (s < hi) ? v[s] : 0.f;
+            if (!mild) {
+#pragma unroll
+              for (int s = 0; s < 16; ++s) v[s] *= exp2f(u.c2 * (float)max(0, p.reverse ? e + s : e + 15 - s)) * p.p_scale;
             }
+          } else if (!mild) {
 #pragma unroll
-            for (int q = 0; q < 16; ++q) wd[q] = bf16x2(v[2 * q], v[2 * q + 1]);
-          } else {
-            // on the diagonal the row factor's exponent is 0 .. -31 (mild decays only)
-            const float rf = p.p_scale * (k == w ? exp2f(u.c2 * (float)(p.reverse ? -lane : lane - 31))
-                                                 : pw[p.reverse ? 32 * k - i : i - 32 * k - 31]);
-            const float2 rf2 = make_float2(rf, rf);
-            if (k == w) {
+            for (int s = 0; s < 16; ++s) v[s] *= exp2f(u.c2 * (float)(p.reverse ? e + s : e + 15 - s)) * p.p_scale;
+          }
+          const float rf = p.p_scale * exp2f(u.c2 * (float)max(e, -15));
 #pragma unroll
-              for (int s = 0; s < 32; ++s) v[s] = (p.reverse ? s >= lane : s <= lane) ? v[s] : 0.f;
+          for (int q = 0; q < 4; ++q) {
+            const float4 cf = *reinterpret_cast<const float4*>(&pcol[4 * q]);
+            float2 f = make_float2(v[4 * q], v[4 * q + 1]), g = make_float2(v[4 * q + 2], v[4 * q + 3]);
+            if (mild) {
+              f = __fmul2_rn(f, __fmul2_rn(make_float2(cf.x, cf.y), make_float2(rf, rf)));
+              g = __fmul2_rn(g, __fmul2_rn(make_float2(cf.z, cf.w), make_float2(rf, rf)));
             }
-            if (32 * k + 32 > L) {  // columns past the last token
-#pragma unroll
-              for (int s = 0; s < 32; ++s) v[s] = 32 * k + s < L ? v[s] : 0.f;
-            }
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const float4 cf = *reinterpret_cast<const float4*>(&pcol[4 * q]);
-              const float2 f = __fmul2_rn(make_float2(v[4 * q], v[4 * q + 1]), __fmul2_rn(make_float2(cf.x, cf.y), rf2));
-              const float2 g = __fmul2_rn(make_float2(v[4 * q + 2], v[4 * q + 3]), __fmul2_rn(make_float2(cf.z, cf.w), rf2));
-              wd[2 * q] = bf16x2(f.x, f.y);
-              wd[2 * q + 1] = bf16x2(g.x, g.y);
-            }
+            wd[2 * q] = bf16x2(f.x, f.y);
+            wd[2 * q + 1] = bf16x2(g.x, g.y);
           }
         }
-        // over scores that this thread has read: blocks 0, 1 to columns 0 .. 31, 2, 3 to 64 .. 95
-        tmem_st16(t_scores + row + (uint32_t)(16 * k + (k < 2 ? 0 : 32)), wd);
+        // over scores that this thread has read
+        tmem_st8(t_scores + row + (uint32_t)(c0 + (c - c0) / 2), wd);
       }
       tc_fence_before();
       __syncwarp();
@@ -485,7 +478,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       const __nv_bfloat16 w1 = __float2bfloat16_rn(wt), w2 = __float2bfloat16_rn(wt - __bfloat162float(w1));
       const __nv_bfloat162 w11 = __halves2bfloat162(w1, w1), w22 = __halves2bfloat162(w2, w2);
       if (bcols > 0) {
-#pragma unroll 4
+#pragma unroll 2
         for (int c = 0; c < 8; ++c) {
           const uint32_t at = (uint32_t)((c ^ (r & 7)) << 4);
           uint4 v = *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(line + at));
