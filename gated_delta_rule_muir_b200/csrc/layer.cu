@@ -156,7 +156,8 @@ int lin_tc(const muir::LinPass* p, int n, const char* name, cudaStream_t s) {
     const uint64_t ra = (uint64_t)q.H * q.da, rc = (uint64_t)q.H * q.dc;
     if ((OUT && !muir_host::make_tmap_bf16_3d(&args.a[i], q.a, ra, (uint64_t)q.T, (uint64_t)q.B, muir::kLtChunk)) ||
         !muir_host::make_tmap_bf16_3d(&args.b[i], q.b, ra, (uint64_t)q.T, (uint64_t)q.B, muir::kLtChunk) ||
-        !muir_host::make_tmap_bf16_3d(&args.c[i], q.c, rc, (uint64_t)q.T, (uint64_t)q.B, muir::kLtChunk))
+        !muir_host::make_tmap_bf16_3d(&args.c[i], q.c, rc, (uint64_t)q.T, (uint64_t)q.B, muir::kLtChunk) ||
+        (OUT && q.dc >= 64 && !muir_host::make_tmap_bf16_3d(&args.o[i], q.out, rc, (uint64_t)q.T, (uint64_t)q.B, 32u)))
       return fail(MUIR_ERR_CUDA, "%s: tensor map encoding failed", name);
     args.p[i] = q;
   }

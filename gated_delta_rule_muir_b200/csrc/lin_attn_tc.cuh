@@ -37,18 +37,18 @@
 // and odd chunks) and one for third parts, which are multiplied first.
 //
 // Roles (896 threads): warp 0 issues TMA copies, warp 1 the MMAs; warps 4..11 mask
-// the scores (one token row, 64 columns per thread); warps 12..19 cut b (half a
-// token row per thread); warps 20..27 keep the state and write outputs (one row, 64
-// columns per thread). The products are issued parts(n), y2(n), y1(n), scores(n+1):
+// the scores (one token row, every other 16 columns per thread); warps 12..19 cut b and
+// write outputs (half a token row per thread; a chunk's outputs after the next one's
+// parts); warps 20..27 keep the state (one row, 64 columns per thread). The products are issued parts(n), y2(n), y1(n), scores(n+1):
 // the parts and y2 run while the scores are masked. The block is launched with 72
-// registers per thread; the warpgroups trade them (40 + 2 x 56 + 2 x 64 + 2 x 112 =
+// registers per thread; the warpgroups trade them (40 + 2 x 56 + 2 x 72 + 2 x 104 =
 // 7 x 72). Hand-offs are mbarriers with bounded waits:
 //   full[s], empty[s]   slot s holds a tile / its readers are done (one commit and
 //                       the eight cutting warps)
 //   scores    scores in TMEM               (MMA -> mask, cut)
 //   weights   masked scores in TMEM        (mask -> MMA)
-//   y2, y     y2 / y1 and y2 in TMEM       (MMA -> state)
-//   y_free    y1 and y2 read               (state -> MMA)
+//   y2, y     y2 / y1 and y2 in TMEM       (MMA -> state / cut)
+//   y_free    y1 and y2 read               (cut -> MMA)
 //   cut       the parts in shared memory   (cut -> MMA)
 //   used3     third parts used             (MMA -> cut; without outputs)
 //   ds        dS in TMEM                   (MMA -> state, cut)
@@ -69,7 +69,8 @@ constexpr uint32_t kLtSmem = 7 * kLtTile + 1024;
 
 constexpr int kLinMaxPasses = 3;
 struct LinTcArgs {
-  CUtensorMap a[kLinMaxPasses], b[kLinMaxPasses], c[kLinMaxPasses];
+  CUtensorMap a[kLinMaxPasses], b[kLinMaxPasses], c[kLinMaxPasses];  // boxes of 64 channels x 128 tokens
+  CUtensorMap o[kLinMaxPasses];  // outputs, 64 x 32; unused for 32 channels
   LinPass p[kLinMaxPasses];
 };
 
@@ -83,14 +84,51 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* tma
       : "memory");
 }
 
+// One box from shared memory to global memory, in this thread's bulk-async group;
+// tokens past T are not written.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* tmap, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
+// Until this thread's committed bulk copies have read their source.
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
 __device__ __forceinline__ void mbar_arrive1(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// Waits of this kernel. Bounded like mbar_wait, with as little code in line as will
+// do (there are some twenty of them, and the roles run at the pace of instruction
+// fetches): the first try decides nearly always, and the time is only looked at
+// every 256 tries after that.
+__device__ __forceinline__ bool is_over(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool lane_wait(uint64_t* bar, uint32_t parity) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1; !is_over(bar, parity); ++it) {
+    if ((it & 255u) == 0) {
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      else if (now - t0 > kWaitLimitNs) { flag_timeout(); return false; }
+    }
+  }
+  return true;
+}
 // A whole warp's wait: every lane gets the same answer, so that the aligned
 // instructions after it are reached by all lanes or by none.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
+  return __all_sync(0xffffffffu, lane_wait(bar, parity)) != 0;
 }
 
 // One MMA with the accumulate flag known at compile time. The issuing thread must
@@ -280,18 +318,19 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
     if (lane == 0) {
       bool ok = true;
       int m = 0;
+      auto map_of = [&](int k) { return k == 0 ? &args.b[pi] : k == TILES - 1 ? &args.c[pi] : &args.a[pi]; };
+      auto width = [&](int k) { return k == TILES - 1 ? p.dc : p.da; };
+      auto first = [&](int n) { return (int)(u.t0 + (int64_t)chunk_at(n) * kLtChunk); };
       for (int n = 0; n < u.chunks && ok; ++n) {
-        const int t = (int)(u.t0 + (int64_t)chunk_at(n) * kLtChunk);
         for (int k = 0; k < TILES && ok; ++k, ++m) {
           const int s = m % SLOTS, turn = m / SLOTS;
-          if (turn > 0) ok = mbar_wait(&empty[s], (uint32_t)(turn - 1) & 1u);
+          if (turn > 0) ok = lane_wait(&empty[s], (uint32_t)(turn - 1) & 1u);
           if (!ok) break;
-          const CUtensorMap* map = k == 0 ? &args.b[pi] : k == TILES - 1 ? &args.c[pi] : &args.a[pi];
-          const int d = k == TILES - 1 ? p.dc : p.da;
+          const int d = width(k);
           const uint32_t dst = base + (uint32_t)s * kLtTile;
           mbar_expect_tx(&full[s], d > 64 ? 2u * kLtBox : kLtBox);
-          tma_load_3d(dst, map, u.h * d, t, u.b, &full[s]);
-          if (d > 64) tma_load_3d(dst + kLtBox, map, u.h * d + 64, t, u.b, &full[s]);
+          for (int x = 0; x < d; x += 64)
+            tma_load_3d(dst + (x ? kLtBox : 0u), map_of(k), u.h * d + x, first(n), u.b, &full[s]);
         }
       }
       // no copy is in flight when the CTA ends, even after a wait that ran out
@@ -304,25 +343,24 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
     // waits' results are the same in every lane and known to be (a vote, a warp
     // reduction), so that the descriptors are formed in uniform registers. Issued
     // from inside a one-lane branch, each product took three to four times as long.
-    const bool leader = elect_one();
     const int chunks = (int)__reduce_max_sync(0xffffffffu, (unsigned)u.chunks);
     const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
     const uint32_t m_scores = tm, m_y1 = tm + 128, m_y2 = tm + 256, m_ds = tm + 384;
+    if (elect_one()) {
     bool ok = true;
     const uint32_t id_scores = idesc_bf16(128, 128, 0, 0), id_y = idesc_bf16(128, p.dc, 0, 1),
                    id_ds = idesc_bf16(128, p.dc, 1, 1);
     auto slot = [&](int m) { return base + (uint32_t)(m % SLOTS) * kLtTile; };
-    auto landed = [&](int m) { return warp_wait(&full[m % SLOTS], (uint32_t)(m / SLOTS) & 1u); };
+    auto landed = [&](int m) { return lane_wait(&full[m % SLOTS], (uint32_t)(m / SLOTS) & 1u); };
     auto scores = [&](int n) {  // a b^T of chunk n; its TMEM columns hold chunk n - 1's weights until y1 is done
       const int m = n * TILES;
-      if (!landed(m) || !landed(m + 1) || (n > 0 && !warp_wait(&b_y, (uint32_t)(n - 1) & 1u))) return false;
+      if (!landed(m) || !landed(m + 1) || (n > 0 && !lane_wait(&b_y, (uint32_t)(n - 1) & 1u))) return false;
       tc_fence_after();
-      if (leader) {
+      {
         lt_product_k<false>(p.da, m_scores, slot(m + 1), slot(m), id_scores);
         mma_commit(&b_scores);
         if (PARTS == 2) mma_commit(&empty[m % SLOTS]);
       }
-      __syncwarp();
       return true;
     };
     if (OUT && chunks > 0) ok = scores(0);
@@ -331,10 +369,10 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       const int mb = n * TILES, ma = mb + 1, mc = mb + TILES - 1;
       const uint32_t bt = slot(mb), ct = slot(mc);
       // c's tile: landed, and its rows past the last token cleared by the cutters
-      ok = landed(mc) && warp_wait(&b_cut, ph) && (n == 0 || warp_wait(&b_dsfree, ph ^ 1u));
+      ok = landed(mc) && lane_wait(&b_cut, ph) && (n == 0 || lane_wait(&b_dsfree, ph ^ 1u));
       if (!ok) break;
       tc_fence_after();
-      if (leader) {
+      {
         if (PARTS == 3) {
           lt_product<8, false, true, true>(m_ds, part3(n, bt), ct, id_ds);
           if (!OUT) mma_commit(&b_used3);
@@ -347,52 +385,51 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
         if (PARTS == 3) mma_commit(&empty[mb % SLOTS]);
         if (!OUT) mma_commit(&empty[mc % SLOTS]);
       }
-      __syncwarp();
       if (OUT) {
-        ok = warp_wait(&b_sready, ph) && (n == 0 || warp_wait(&b_yfree, ph ^ 1u));
+        ok = lane_wait(&b_sready, ph) && (n == 0 || lane_wait(&b_yfree, ph ^ 1u));
         if (!ok) break;
         tc_fence_after();
-        if (leader) {
+        {
           lt_product_k<true>(p.da, m_y2, slot(ma), s_tile, id_y);
           mma_commit(&b_y2);
           mma_commit(&empty[ma % SLOTS]);
         }
-        __syncwarp();
-        ok = warp_wait(&b_weights, ph);
+        }
+      if (OUT) {
+        ok = lane_wait(&b_weights, ph);
         if (!ok) break;
         tc_fence_after();
-        if (leader) {
+        {
           const uint32_t cd = lt_desc(ct, kLtBox);
           mma_step_ta<false>(m_y1, m_scores, cd, id_y);
 #pragma unroll
           for (int j = 1; j < 8; ++j)
-            mma_step_ta<true>(m_y1, m_scores + (uint32_t)(j < 4 ? 8 * j : 32 + 8 * j), cd + lt_mnstep(j), id_y);
+            mma_step_ta<true>(m_y1, m_scores + (uint32_t)(16 * j), cd + lt_mnstep(j), id_y);
           mma_commit(&b_y);
           mma_commit(&empty[mc % SLOTS]);
         }
-        __syncwarp();
-        if (n + 1 < chunks) ok = scores(n + 1);
+          if (n + 1 < chunks) ok = scores(n + 1);
       }
     }
     // every issued product has completed when the CTA ends: the last chunk's commits
     // are waited for here, or after a wait that ran out one more commit is
     if (ok) {
       if (chunks > 0) {
-        warp_wait(&b_ds, (uint32_t)(chunks - 1) & 1u);
-        if (OUT) warp_wait(&b_y, (uint32_t)(chunks - 1) & 1u);
+        lane_wait(&b_ds, (uint32_t)(chunks - 1) & 1u);
+        if (OUT) lane_wait(&b_y, (uint32_t)(chunks - 1) & 1u);
       }
     } else {
-      if (leader) mma_commit(&b_ds);
-      __syncwarp();
+      mma_commit(&b_ds);
       mbar_wait_for(&b_ds, 0u, 1000000ull);
       mbar_wait_for(&b_ds, 1u, 1000000ull);
     }
     }
+    }
   } else if (warp < 12) {
-    // ---- mask: thread = token row i of the chunk, 64 of its columns -------------------------
+    // ---- mask: thread = token row i of the chunk, every other 16 columns -------------------------
     regs_dec<56>();
     if constexpr (OUT) {
-    const int w = warp & 3, i = w * 32 + lane, c0 = warp < 8 ? 0 : 64;
+    const int w = warp & 3, i = w * 32 + lane, c0 = warp < 8 ? 0 : 16;
     const uint32_t row = tmem_lane_base(warp);
     // 16 columns at a time in one short loop (an unrolled body of this size runs at the
     // pace of instruction fetches). lambda^gap = (row factor) (column factor), the
@@ -407,12 +444,13 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       ok = warp_wait(&b_scores, ph);
       if (!ok) break;
       tc_fence_after();
+      auto skip = [&](int c) { return p.reverse ? c + 15 < 32 * w : c > 32 * w + 31; };  // nothing counts for the warp's rows
 #pragma unroll 1
-      for (int c = c0; c < c0 + 64; c += 16) {
+      for (int c = c0; c < 128; c += 32) {
         // columns lo .. hi - 1 of the 16 count
         const int lo = p.reverse ? i - c : 0, hi = (p.reverse ? L : (i + 1 < L ? i + 1 : L)) - c;
         uint32_t wd[8];
-        if (p.reverse ? c + 15 < 32 * w : c > 32 * w + 31) {  // none of any row of the warp
+        if (skip(c)) {
 #pragma unroll
           for (int q = 0; q < 8; ++q) wd[q] = 0u;
         } else {
@@ -423,13 +461,10 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
             // dropped, not multiplied by zero: a score that does not count may be anything
 #pragma unroll
             for (int s = 0; s < 16; ++s) v[s] = (s >= lo) & (s < hi) ? v[s] : 0.f;
-            if (!mild) {
+          }
+          if (!mild) {
 #pragma unroll
-              for (int s = 0; s < 16; ++s) v[s] *= exp2f(u.c2 * (float)max(0, p.reverse ? e + s : e + 15 - s)) * p.p_scale;
-            }
-          } else if (!mild) {
-#pragma unroll
-            for (int s = 0; s < 16; ++s) v[s] *= exp2f(u.c2 * (float)(p.reverse ? e + s : e + 15 - s)) * p.p_scale;
+            for (int s = 0; s < 16; ++s) v[s] *= p.p_scale * pw[max(0, p.reverse ? e + s : e + 15 - s)];
           }
           const float rf = p.p_scale * exp2f(u.c2 * (float)max(e, -15));
 #pragma unroll
@@ -444,8 +479,8 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
             wd[2 * q + 1] = bf16x2(g.x, g.y);
           }
         }
-        // over scores that this thread has read
-        tmem_st8(t_scores + row + (uint32_t)(c0 + (c - c0) / 2), wd);
+        // over the first half of the scores they come from
+        tmem_st8(t_scores + row + (uint32_t)c, wd);
       }
       tc_fence_before();
       __syncwarp();
@@ -453,26 +488,85 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
     }
     }
   } else if (warp < 20) {
-    // ---- cut b: thread = half a token row ---------------------------------------------------
-    regs_dec<64>();
+    // ---- cut b, outputs: thread = half a token row ---------------------------------------------
     const int half = (warp - 12) >> 2;     // columns 64 half ..
     const int r = (warp & 3) * 32 + lane;  // token row
     const int bcols = p.da - 64 * half < 64 ? p.da - 64 * half : 64;  // at most 0: none
     const uint32_t place = (uint32_t)half * kLtBox + (uint32_t)r * 128u;
+    __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(p.out) + (((int64_t)u.b * p.T + u.t0) * p.H + u.h) * p.dc;
+    const int64_t pitch = (int64_t)p.H * p.dc;
+    if constexpr (OUT) {  // padded tokens of this segment: zeros
+      const int64_t end = (u.t0 + p.seglen < p.T ? p.seglen : p.T - u.t0);
+      const int pieces = p.dc / 8;
+      for (int64_t x = u.valid * pieces + tid - 384; x < end * pieces; x += 256)
+        *reinterpret_cast<uint4*>(out + (x / pieces) * pitch + (x % pieces) * 8) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    const uint32_t row = tmem_lane_base(warp);
+    // outputs of chunk n: row r, columns 64 half .. They are laid down in c's tile, which
+    // y1 has read by then, and copied out by the warp's own TMA store, in whole lines
+    // (a token row per thread stored directly takes a pass of the load-store unit per
+    // row and instruction: 1700 of the chunk's 7000 cycles). 32 channels are half a
+    // box; those go directly.
+    const bool boxed = p.dc >= 64;
+    auto outputs = [&](int n) {
+      const int64_t r0 = (int64_t)chunk_at(n) * kLtChunk;
+      const int L = (int)(u.valid - r0 < kLtChunk ? u.valid - r0 : kLtChunk);
+      if (!warp_wait(&b_y, (uint32_t)n & 1u)) return false;
+      tc_fence_after();
+      const float rw = p.o_scale * (p.reverse ? pw[r < L ? L - 1 - r : 0] : exp2f(u.c2 * (float)(r + 1)));
+      const float2 rw2 = make_float2(rw, rw);
+      const uint32_t stage = base + (uint32_t)((n * TILES + TILES - 1) % SLOTS) * kLtTile + place;
+#pragma unroll 1
+      for (int c = 64 * half; c < 64 * half + 64 && c < p.dc; c += 16) {
+        float y1[16], y2[16];
+        tmem_ld16x2(t_y1 + row + (uint32_t)c, t_y2 + row + (uint32_t)c, y1, y2);
+        uint32_t o[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float2 y = __ffma2_rn(rw2, make_float2(y2[2 * q], y2[2 * q + 1]), make_float2(y1[2 * q], y1[2 * q + 1]));
+          o[q] = r < L ? bf16x2(y.x, y.y) : 0u;  // padded tokens: zeros
+        }
+        if (boxed) {
+          const uint32_t k = (uint32_t)((c & 63) >> 3);
+          sts128(stage + (((k ^ (uint32_t)(r & 7))) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+          sts128(stage + ((((k + 1) ^ (uint32_t)(r & 7))) << 4), make_uint4(o[4], o[5], o[6], o[7]));
+        } else if (r < L) {
+          stg_bf16x16(out + (r0 + r) * pitch + c, o);
+        }
+      }
+      tc_fence_before();
+      if (boxed) fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive1(&b_yfree);
+        if (boxed && 64 * half < p.dc) {
+          tma_store_3d(&args.o[pi], stage, u.h * p.dc + 64 * half, (int)(u.t0 + r0) + r, u.b);
+          bulk_commit();
+        }
+      }
+      return true;
+    };
+    // c's tile of chunk n may be filled again
+    auto release_c = [&](int n) {
+      if (lane == 0) {
+        bulk_wait_read();
+        mbar_arrive1(&empty[(n * TILES + TILES - 1) % SLOTS]);
+      }
+    };
     bool ok = true;
-    for (int n = 0; n < u.chunks && ok; ++n) {
+    auto parts = [&](int n) {
       const int64_t r0 = (int64_t)chunk_at(n) * kLtChunk;
       const int L = (int)(u.valid - r0 < kLtChunk ? u.valid - r0 : kLtChunk);
       const int mb = n * TILES, mc = mb + TILES - 1;
       const uint32_t bt = base + (uint32_t)(mb % SLOTS) * kLtTile;
       const uint32_t line = bt + place, l1 = part1(n, bt) + place, l2 = part2(n, bt) + place, l3 = part3(n, bt) + place;
       const float wt = r < L ? p.u_scale * exp2f(u.c2 * (float)(p.reverse ? r + 1 : L - 1 - r)) : 0.f;
-      ok = warp_wait(&full[mb % SLOTS], (uint32_t)(mb / SLOTS) & 1u);
+      bool ok = warp_wait(&full[mb % SLOTS], (uint32_t)(mb / SLOTS) & 1u);
       if (L < kLtChunk) ok = ok && warp_wait(&full[mc % SLOTS], (uint32_t)(mc / SLOTS) & 1u);
       // the tiles of the last parts have been used; before third parts go over b, the scores have been formed
       if (n > 0) ok = ok && warp_wait(OUT ? &b_ds : &b_used3, (uint32_t)(n - 1) & 1u);
       if (OUT && PARTS == 3) ok = ok && warp_wait(&b_scores, (uint32_t)n & 1u);
-      if (!ok) break;
+      if (!ok) return false;
       // packed bf16, two parts: with the weight as w1 + w2, p1 = b w1 rounded, and
       // p2 = (b w1 - p1) + b w2, the bracket exact, rounded once
       const __nv_bfloat16 w1 = __float2bfloat16_rn(wt), w2 = __float2bfloat16_rn(wt - __bfloat162float(w1));
@@ -523,12 +617,22 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       __syncwarp();
       if (lane == 0) {
         mbar_arrive1(&b_cut);
-        for (int m = mb; m <= mc; ++m) mbar_arrive1(&empty[m % SLOTS]);
+        for (int m = mb; m < mc; ++m) mbar_arrive1(&empty[m % SLOTS]);
+        if (!OUT) mbar_arrive1(&empty[mc % SLOTS]);
+      }
+      return true;
+    };
+    for (int n = 0; n < u.chunks + (OUT ? 1 : 0) && ok; ++n) {
+      if (n < u.chunks) ok = parts(n);
+      if (OUT && ok && n > 0) {  // the next chunk's parts come first
+        ok = outputs(n - 1);
+        release_c(n - 1);
       }
     }
+    if (OUT && lane == 0) bulk_wait_all();
   } else {
-    // ---- the state and outputs: thread = row r, columns 64 half .. ---------------------------------
-    regs_inc<112>();
+    // ---- the state: thread = row r, columns 64 half .. ---------------------------------------------
+    regs_inc<104>();
     const int half = (warp - 20) >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t row = tmem_lane_base(warp);
@@ -544,10 +648,16 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
         else if (p.init) { src = p.init + (int64_t)u.bh * nstate; tr = p.init_t; }
       }
 #pragma unroll
-      for (int j = 0; j < 64; ++j) {
-        S[j] = 0.f;
-        if (src && mine && j < scols)
-          S[j] = tr ? __ldg(src + (int64_t)(64 * half + j) * p.da + r) : __ldg(src + (int64_t)r * p.dc + 64 * half + j);
+      for (int j = 0; j < 64; ++j) S[j] = 0.f;
+      if (src && mine) {
+        const int step = tr ? p.da : 1;  // between columns
+        src += tr ? (int64_t)(64 * half) * p.da + r : (int64_t)r * p.dc + 64 * half;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) S[j] = __ldg(src + j * step);
+        if (scols == 64) {
+#pragma unroll
+          for (int j = 32; j < 64; ++j) S[j] = __ldg(src + j * step);
+        }
       }
     }
     auto put_state = [&]() {  // S's operand copy
@@ -566,47 +676,16 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       __syncwarp();
       if (lane == 0) mbar_arrive1(&b_sready);
     };
-    if constexpr (OUT) put_state();
-    __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(p.out) + (((int64_t)u.b * p.T + u.t0) * p.H + u.h) * p.dc;
-    const int64_t pitch = (int64_t)p.H * p.dc;
-    if constexpr (OUT) {  // padded tokens of this segment: zeros
-      const int64_t end = (u.t0 + p.seglen < p.T ? p.seglen : p.T - u.t0);
-      const int pieces = p.dc / 8;
-      for (int64_t x = u.valid * pieces + tid - 640; x < end * pieces; x += 256)
-        *reinterpret_cast<uint4*>(out + (x / pieces) * pitch + (x % pieces) * 8) = make_uint4(0u, 0u, 0u, 0u);
-    }
-    // outputs of chunk n: row r, columns 64 half ..
-    auto outputs = [&](int n) {
-      const int64_t r0 = (int64_t)chunk_at(n) * kLtChunk;
-      const int L = (int)(u.valid - r0 < kLtChunk ? u.valid - r0 : kLtChunk);
-      if (!warp_wait(&b_y, (uint32_t)n & 1u)) return false;
-      tc_fence_after();
-      const float rw = p.o_scale * (p.reverse ? pw[r < L ? L - 1 - r : 0] : exp2f(u.c2 * (float)(r + 1)));
-      const float2 rw2 = make_float2(rw, rw);
-#pragma unroll 1
-      for (int c = 64 * half; c < 64 * half + 64 && c < p.dc; c += 16) {
-        float y1[16], y2[16];
-        tmem_ld16x2(t_y1 + row + (uint32_t)c, t_y2 + row + (uint32_t)c, y1, y2);
-        if (r < L) {
-          uint32_t o[8];
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float2 y = __ffma2_rn(rw2, make_float2(y2[2 * q], y2[2 * q + 1]), make_float2(y1[2 * q], y1[2 * q + 1]));
-            o[q] = bf16x2(y.x, y.y);
-          }
-          stg_bf16x16(out + (r0 + r) * pitch + c, o);
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive1(&b_yfree);
-      return true;
-    };
     bool ok = true;
     for (int n = 0; n < u.chunks && ok; ++n) {
       const int64_t r0 = (int64_t)chunk_at(n) * kLtChunk;
       const int L = (int)(u.valid - r0 < kLtChunk ? u.valid - r0 : kLtChunk);
       const LinDecay wl = lin_decay(u.c2, L);
+      if (OUT) {
+        if (n > 0) ok = warp_wait(&b_y2, (uint32_t)(n - 1) & 1u);  // the last copy has been used
+        if (!ok) break;
+        put_state();
+      }
       ok = warp_wait(&b_ds, (uint32_t)n & 1u);
       if (!ok) break;
       tc_fence_after();
@@ -629,12 +708,6 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive1(&b_dsfree);
-      if (OUT && n + 1 < u.chunks) {
-        ok = warp_wait(&b_y2, (uint32_t)n & 1u);  // the last copy has been used
-        if (!ok) break;
-        put_state();
-      }
-      if (OUT) ok = outputs(n);
     }
     float* dst = nullptr;
     if constexpr (!OUT) dst = p.seg + ((int64_t)u.bh * p.nseg + u.seg) * nstate;
