@@ -37,18 +37,18 @@
 // and odd chunks) and one for third parts, which are multiplied first.
 //
 // Roles (896 threads): warp 0 issues TMA copies, warp 1 the MMAs; warps 4..11 mask
-// the scores (one token row, every other 16 columns per thread); warps 12..19 cut b and
-// write outputs (half a token row per thread; a chunk's outputs after the next one's
-// parts); warps 20..27 keep the state (one row, 64 columns per thread). The products are issued parts(n), y2(n), y1(n), scores(n+1):
+// the scores (one token row, every other 16 columns per thread); warps 12..19 cut b
+// (half a token row per thread); warps 20..27 keep the state and write outputs (one
+// row, 64 columns per thread). The products are issued parts(n), y2(n), y1(n), scores(n+1):
 // the parts and y2 run while the scores are masked. The block is launched with 72
-// registers per thread; the warpgroups trade them (40 + 2 x 56 + 2 x 72 + 2 x 104 =
+// registers per thread; the warpgroups trade them (40 + 2 x 56 + 2 x 64 + 2 x 112 =
 // 7 x 72). Hand-offs are mbarriers with bounded waits:
 //   full[s], empty[s]   slot s holds a tile / its readers are done (one commit and
 //                       the eight cutting warps)
 //   scores    scores in TMEM               (MMA -> mask, cut)
 //   weights   masked scores in TMEM        (mask -> MMA)
-//   y2, y     y2 / y1 and y2 in TMEM       (MMA -> state / cut)
-//   y_free    y1 and y2 read               (cut -> MMA)
+//   y2, y     y2 / y1 and y2 in TMEM       (MMA -> state)
+//   y_free    y1 and y2 read               (state -> MMA)
 //   cut       the parts in shared memory   (cut -> MMA)
 //   used3     third parts used             (MMA -> cut; without outputs)
 //   ds        dS in TMEM                   (MMA -> state, cut)
@@ -488,85 +488,26 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
     }
     }
   } else if (warp < 20) {
-    // ---- cut b, outputs: thread = half a token row ---------------------------------------------
+    // ---- cut b: thread = half a token row --------------------------------------------------------
+    regs_dec<64>();
     const int half = (warp - 12) >> 2;     // columns 64 half ..
     const int r = (warp & 3) * 32 + lane;  // token row
     const int bcols = p.da - 64 * half < 64 ? p.da - 64 * half : 64;  // at most 0: none
     const uint32_t place = (uint32_t)half * kLtBox + (uint32_t)r * 128u;
-    __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(p.out) + (((int64_t)u.b * p.T + u.t0) * p.H + u.h) * p.dc;
-    const int64_t pitch = (int64_t)p.H * p.dc;
-    if constexpr (OUT) {  // padded tokens of this segment: zeros
-      const int64_t end = (u.t0 + p.seglen < p.T ? p.seglen : p.T - u.t0);
-      const int pieces = p.dc / 8;
-      for (int64_t x = u.valid * pieces + tid - 384; x < end * pieces; x += 256)
-        *reinterpret_cast<uint4*>(out + (x / pieces) * pitch + (x % pieces) * 8) = make_uint4(0u, 0u, 0u, 0u);
-    }
-    const uint32_t row = tmem_lane_base(warp);
-    // outputs of chunk n: row r, columns 64 half .. They are laid down in c's tile, which
-    // y1 has read by then, and copied out by the warp's own TMA store, in whole lines
-    // (a token row per thread stored directly takes a pass of the load-store unit per
-    // row and instruction: 1700 of the chunk's 7000 cycles). 32 channels are half a
-    // box; those go directly.
-    const bool boxed = p.dc >= 64;
-    auto outputs = [&](int n) {
-      const int64_t r0 = (int64_t)chunk_at(n) * kLtChunk;
-      const int L = (int)(u.valid - r0 < kLtChunk ? u.valid - r0 : kLtChunk);
-      if (!warp_wait(&b_y, (uint32_t)n & 1u)) return false;
-      tc_fence_after();
-      const float rw = p.o_scale * (p.reverse ? pw[r < L ? L - 1 - r : 0] : exp2f(u.c2 * (float)(r + 1)));
-      const float2 rw2 = make_float2(rw, rw);
-      const uint32_t stage = base + (uint32_t)((n * TILES + TILES - 1) % SLOTS) * kLtTile + place;
-#pragma unroll 1
-      for (int c = 64 * half; c < 64 * half + 64 && c < p.dc; c += 16) {
-        float y1[16], y2[16];
-        tmem_ld16x2(t_y1 + row + (uint32_t)c, t_y2 + row + (uint32_t)c, y1, y2);
-        uint32_t o[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float2 y = __ffma2_rn(rw2, make_float2(y2[2 * q], y2[2 * q + 1]), make_float2(y1[2 * q], y1[2 * q + 1]));
-          o[q] = r < L ? bf16x2(y.x, y.y) : 0u;  // padded tokens: zeros
-        }
-        if (boxed) {
-          const uint32_t k = (uint32_t)((c & 63) >> 3);
-          sts128(stage + (((k ^ (uint32_t)(r & 7))) << 4), make_uint4(o[0], o[1], o[2], o[3]));
-          sts128(stage + ((((k + 1) ^ (uint32_t)(r & 7))) << 4), make_uint4(o[4], o[5], o[6], o[7]));
-        } else if (r < L) {
-          stg_bf16x16(out + (r0 + r) * pitch + c, o);
-        }
-      }
-      tc_fence_before();
-      if (boxed) fence_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive1(&b_yfree);
-        if (boxed && 64 * half < p.dc) {
-          tma_store_3d(&args.o[pi], stage, u.h * p.dc + 64 * half, (int)(u.t0 + r0) + r, u.b);
-          bulk_commit();
-        }
-      }
-      return true;
-    };
-    // c's tile of chunk n may be filled again
-    auto release_c = [&](int n) {
-      if (lane == 0) {
-        bulk_wait_read();
-        mbar_arrive1(&empty[(n * TILES + TILES - 1) % SLOTS]);
-      }
-    };
     bool ok = true;
-    auto parts = [&](int n) {
+    for (int n = 0; n < u.chunks && ok; ++n) {
       const int64_t r0 = (int64_t)chunk_at(n) * kLtChunk;
       const int L = (int)(u.valid - r0 < kLtChunk ? u.valid - r0 : kLtChunk);
       const int mb = n * TILES, mc = mb + TILES - 1;
       const uint32_t bt = base + (uint32_t)(mb % SLOTS) * kLtTile;
       const uint32_t line = bt + place, l1 = part1(n, bt) + place, l2 = part2(n, bt) + place, l3 = part3(n, bt) + place;
       const float wt = r < L ? p.u_scale * exp2f(u.c2 * (float)(p.reverse ? r + 1 : L - 1 - r)) : 0.f;
-      bool ok = warp_wait(&full[mb % SLOTS], (uint32_t)(mb / SLOTS) & 1u);
+      ok = warp_wait(&full[mb % SLOTS], (uint32_t)(mb / SLOTS) & 1u);
       if (L < kLtChunk) ok = ok && warp_wait(&full[mc % SLOTS], (uint32_t)(mc / SLOTS) & 1u);
       // the tiles of the last parts have been used; before third parts go over b, the scores have been formed
       if (n > 0) ok = ok && warp_wait(OUT ? &b_ds : &b_used3, (uint32_t)(n - 1) & 1u);
       if (OUT && PARTS == 3) ok = ok && warp_wait(&b_scores, (uint32_t)n & 1u);
-      if (!ok) return false;
+      if (!ok) break;
       // packed bf16, two parts: with the weight as w1 + w2, p1 = b w1 rounded, and
       // p2 = (b w1 - p1) + b w2, the bracket exact, rounded once
       const __nv_bfloat16 w1 = __float2bfloat16_rn(wt), w2 = __float2bfloat16_rn(wt - __bfloat162float(w1));
@@ -620,19 +561,10 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
         for (int m = mb; m < mc; ++m) mbar_arrive1(&empty[m % SLOTS]);
         if (!OUT) mbar_arrive1(&empty[mc % SLOTS]);
       }
-      return true;
-    };
-    for (int n = 0; n < u.chunks + (OUT ? 1 : 0) && ok; ++n) {
-      if (n < u.chunks) ok = parts(n);
-      if (OUT && ok && n > 0) {  // the next chunk's parts come first
-        ok = outputs(n - 1);
-        release_c(n - 1);
-      }
     }
-    if (OUT && lane == 0) bulk_wait_all();
   } else {
-    // ---- the state: thread = row r, columns 64 half .. ---------------------------------------------
-    regs_inc<104>();
+    // ---- the state and outputs: thread = row r, columns 64 half .. -----------------------------------
+    regs_inc<112>();
     const int half = (warp - 20) >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t row = tmem_lane_base(warp);
@@ -676,39 +608,108 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       __syncwarp();
       if (lane == 0) mbar_arrive1(&b_sready);
     };
-    bool ok = true;
-    for (int n = 0; n < u.chunks && ok; ++n) {
+    __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(p.out) + (((int64_t)u.b * p.T + u.t0) * p.H + u.h) * p.dc;
+    const int64_t pitch = (int64_t)p.H * p.dc;
+    if constexpr (OUT) {  // padded tokens of this segment: zeros
+      const int64_t end = (u.t0 + p.seglen < p.T ? p.seglen : p.T - u.t0);
+      const int pieces = p.dc / 8;
+      for (int64_t x = u.valid * pieces + tid - 640; x < end * pieces; x += 256)
+        *reinterpret_cast<uint4*>(out + (x / pieces) * pitch + (x % pieces) * 8) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    // outputs of chunk n: row r, columns 64 half .. They are laid down in c's tile, which
+    // y1 has read by then, and copied out by the warp's own TMA store, in whole lines
+    // (a token row per thread stored directly takes a pass of the load-store unit per
+    // row and instruction: 1700 of the chunk's 7000 cycles). 32 channels are half a
+    // box; those go directly.
+    const bool boxed = p.dc >= 64;
+    auto outputs = [&](int n) {
       const int64_t r0 = (int64_t)chunk_at(n) * kLtChunk;
       const int L = (int)(u.valid - r0 < kLtChunk ? u.valid - r0 : kLtChunk);
-      const LinDecay wl = lin_decay(u.c2, L);
-      if (OUT) {
-        if (n > 0) ok = warp_wait(&b_y2, (uint32_t)(n - 1) & 1u);  // the last copy has been used
-        if (!ok) break;
-        put_state();
-      }
-      ok = warp_wait(&b_ds, (uint32_t)n & 1u);
-      if (!ok) break;
+      if (!warp_wait(&b_y, (uint32_t)n & 1u)) return false;
       tc_fence_after();
+      const float rw = p.o_scale * (p.reverse ? pw[r < L ? L - 1 - r : 0] : exp2f(u.c2 * (float)(r + 1)));
+      const float2 rw2 = make_float2(rw, rw);
+      const uint32_t stage = base + (uint32_t)((n * TILES + TILES - 1) % SLOTS) * kLtTile + (uint32_t)half * kLtBox + (uint32_t)r * 128u;
+#pragma unroll 1
+      for (int c = 64 * half; c < 64 * half + 64 && c < p.dc; c += 16) {
+        float y1[16], y2[16];
+        tmem_ld16x2(t_y1 + row + (uint32_t)c, t_y2 + row + (uint32_t)c, y1, y2);
+        uint32_t o[8];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (64 * half + 16 * q < p.dc) {  // whole warps
-          float d[16];
-          tmem_ld16(t_ds + row + (uint32_t)(64 * half + 16 * q), d);
-          const float2 g = make_float2(wl.g, wl.g), e = make_float2(wl.e, wl.e);
-#pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            float* s2 = S + 16 * q + j;
-            const float2 old = make_float2(s2[0], s2[1]);
-            const float2 now = __ffma2_rn(g, old, __ffma2_rn(e, old, make_float2(d[j], d[j + 1])));
-            s2[0] = now.x;
-            s2[1] = now.y;
-          }
+        for (int q = 0; q < 8; ++q) {
+          const float2 y = __ffma2_rn(rw2, make_float2(y2[2 * q], y2[2 * q + 1]), make_float2(y1[2 * q], y1[2 * q + 1]));
+          o[q] = r < L ? bf16x2(y.x, y.y) : 0u;  // padded tokens: zeros
+        }
+        if (boxed) {
+          const uint32_t k = (uint32_t)((c & 63) >> 3);
+          sts128(stage + (((k ^ (uint32_t)(r & 7))) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+          sts128(stage + ((((k + 1) ^ (uint32_t)(r & 7))) << 4), make_uint4(o[4], o[5], o[6], o[7]));
+        } else if (r < L) {
+          stg_bf16x16(out + (r0 + r) * pitch + c, o);
         }
       }
       tc_fence_before();
+      if (boxed) fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive1(&b_dsfree);
+      if (lane == 0) {
+        mbar_arrive1(&b_yfree);
+        if (boxed && 64 * half < p.dc) {
+          tma_store_3d(&args.o[pi], stage, u.h * p.dc + 64 * half, (int)(u.t0 + r0) + r, u.b);
+          bulk_commit();
+        }
+      }
+      return true;
+    };
+    // c's tile of chunk n may be filled again
+    auto release_c = [&](int n) {
+      if (lane == 0) {
+        bulk_wait_read();
+        mbar_arrive1(&empty[(n * TILES + TILES - 1) % SLOTS]);
+      }
+    };
+    bool ok = true;
+    // step n: S after chunk n - 1, its operand copy for chunk n, the outputs of chunk n - 1
+    for (int n = OUT ? 0 : 1; n <= u.chunks && ok; ++n) {
+      if (n > 0) {
+        const int64_t r0 = (int64_t)chunk_at(n - 1) * kLtChunk;
+        const int L = (int)(u.valid - r0 < kLtChunk ? u.valid - r0 : kLtChunk);
+        const LinDecay wl = lin_decay(u.c2, L);
+        ok = warp_wait(&b_ds, (uint32_t)(n - 1) & 1u);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (64 * half + 16 * q < p.dc) {  // whole warps
+            float d[16];
+            tmem_ld16(t_ds + row + (uint32_t)(64 * half + 16 * q), d);
+            const float2 g = make_float2(wl.g, wl.g), e = make_float2(wl.e, wl.e);
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              float* s2 = S + 16 * q + j;
+              const float2 old = make_float2(s2[0], s2[1]);
+              const float2 now = __ffma2_rn(g, old, __ffma2_rn(e, old, make_float2(d[j], d[j + 1])));
+              s2[0] = now.x;
+              s2[1] = now.y;
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive1(&b_dsfree);
+      }
+      if constexpr (OUT) {
+        if (n < u.chunks) {
+          if (n > 0) ok = warp_wait(&b_y2, (uint32_t)(n - 1) & 1u);  // the last copy has been used
+          if (!ok) break;
+          put_state();
+        }
+        if (n > 0) {
+          ok = outputs(n - 1);
+          release_c(n - 1);
+        }
+      }
     }
+    if (OUT && lane == 0) bulk_wait_all();
     float* dst = nullptr;
     if constexpr (!OUT) dst = p.seg + ((int64_t)u.bh * p.nseg + u.seg) * nstate;
     else if (p.fin && p.nseg == 1) dst = p.fin + (int64_t)u.bh * nstate;
