@@ -66,8 +66,7 @@ bool lin_use_tc(const muir_lin_args* a) {
 // segments' own states where there is more than one (which read two of three
 // operands again: half as much again) and the walk over them.
 //
-// CUDA cores: two CTAs for each SM, at least 8 runs per segment so that its start
-// (a state in and out) stays small.
+// CUDA cores: two CTAs for each SM, at least 2 runs per segment.
 LinPlan lin_plan(const muir_lin_args* a, int passes) {
   LinPlan pl{lin_use_tc(a), 1, 0};
   const int64_t run = pl.tc ? muir::kLtChunk : muir::kLinRun;
@@ -86,9 +85,9 @@ LinPlan lin_plan(const muir_lin_args* a, int passes) {
     }
   } else {
     const int dmin = a->dk < a->dv && passes > 1 ? a->dk : a->dv;
-    const int64_t units = a->B * a->H * (dmin / 32);
+    const int64_t units = a->B * a->H * (dmin / 32) * passes;
     n = (2 * kSMs + units - 1) / units;
-    if (n > runs / 8) n = runs / 8;
+    if (n > runs / 2) n = runs / 2;
     if (n < 1) n = 1;
   }
   const int64_t per = (runs + n - 1) / n;
@@ -129,23 +128,38 @@ int set_smem(K kernel, size_t bytes) {
   return MUIR_OK;
 }
 
+// CUDA-core passes: those with the same da share a launch.
 template <int DA, typename T, bool OUT>
-int lin_simt(const muir::LinPass& p, const char* name, cudaStream_t s) {
-  const int64_t blocks = (int64_t)p.B * p.H * p.nseg * (p.dc / 32);
+int lin_simt(const muir::LinSimtArgs& args, int n, const char* name, cudaStream_t s) {
+  int64_t blocks = 0;
+  for (int i = 0; i < n; ++i) {
+    const muir::LinPass& p = args.p[i];
+    const int64_t own = (int64_t)p.B * p.H * p.nseg * (p.dc / 32);
+    blocks = own > blocks ? own : blocks;
+  }
   if (blocks > kMaxBlocks) return fail(MUIR_ERR_UNSUPPORTED, "%s: too many blocks", name);
   if (int rc = set_smem(muir::lin_simt_kernel<DA, T, OUT>, sizeof(muir::LinSmem<DA>))) return rc;
   LaunchScope l(name, s);
-  muir::lin_simt_kernel<DA, T, OUT><<<(unsigned)blocks, 256, sizeof(muir::LinSmem<DA>), s>>>(p);
+  muir::lin_simt_kernel<DA, T, OUT><<<dim3((unsigned)blocks, (unsigned)n), 256, sizeof(muir::LinSmem<DA>), s>>>(args);
   return check_launch(name);
 }
 template <typename T, bool OUT>
-int lin_simt_da(const muir::LinPass& p, const char* name, cudaStream_t s) {
-  return p.da == 32 ? lin_simt<32, T, OUT>(p, name, s) : p.da == 64 ? lin_simt<64, T, OUT>(p, name, s)
-                                                                     : lin_simt<128, T, OUT>(p, name, s);
+int lin_simt_passes(const muir::LinPass* p, int n, const char* name, cudaStream_t s) {
+  for (const int da : {32, 64, 128}) {
+    muir::LinSimtArgs args{};
+    int m = 0;
+    for (int i = 0; i < n; ++i)
+      if (p[i].da == da) args.p[m++] = p[i];
+    if (m == 0) continue;
+    const int rc = da == 32 ? lin_simt<32, T, OUT>(args, m, name, s)
+                 : da == 64 ? lin_simt<64, T, OUT>(args, m, name, s) : lin_simt<128, T, OUT>(args, m, name, s);
+    if (rc) return rc;
+  }
+  return MUIR_OK;
 }
-int lin_simt_pass(const muir::LinPass& p, int dtype, bool out, const char* name, cudaStream_t s) {
-  if (dtype == MUIR_BF16) return out ? lin_simt_da<bf16, true>(p, name, s) : lin_simt_da<bf16, false>(p, name, s);
-  return out ? lin_simt_da<float, true>(p, name, s) : lin_simt_da<float, false>(p, name, s);
+template <bool OUT>
+int lin_simt_all(const muir::LinPass* p, int n, int dtype, const char* name, cudaStream_t s) {
+  return dtype == MUIR_BF16 ? lin_simt_passes<bf16, OUT>(p, n, name, s) : lin_simt_passes<float, OUT>(p, n, name, s);
 }
 
 template <bool OUT, int PARTS>
@@ -175,12 +189,8 @@ int lin_run(const LinPlan& pl, int dtype, const muir::LinPass* states, int ns, c
             const char* name, cudaStream_t s) {
   int rc = MUIR_OK;
   if (pl.nseg > 1) {
-    if (pl.tc) {
-      if ((rc = lin_tc<false, 3>(states, ns, "lin_state", s))) return rc;
-    } else {
-      for (int i = 0; i < ns; ++i)
-        if ((rc = lin_simt_pass(states[i], dtype, false, "lin_state", s))) return rc;
-    }
+    rc = pl.tc ? lin_tc<false, 3>(states, ns, "lin_state", s) : lin_simt_all<false>(states, ns, dtype, "lin_state", s);
+    if (rc) return rc;
     muir::LinCombineArgs ca{};
     for (int i = 0; i < ns; ++i) ca.p[i] = states[i];
     const muir::LinPass& p = states[0];
@@ -194,9 +204,7 @@ int lin_run(const LinPlan& pl, int dtype, const muir::LinPass* states, int ns, c
     for (int i = 0; i < no; ++i) fin = fin || (pl.nseg == 1 && outs[i].fin);
     return fin ? lin_tc<true, 3>(outs, no, name, s) : lin_tc<true, 2>(outs, no, name, s);
   }
-  for (int i = 0; i < no; ++i)
-    if ((rc = lin_simt_pass(outs[i], dtype, true, name, s))) return rc;
-  return MUIR_OK;
+  return lin_simt_all<true>(outs, no, dtype, name, s);
 }
 
 muir::LinPass lin_pass(const muir_lin_args* x, const LinPlan& pl, int da, int dc) {

@@ -125,6 +125,11 @@ __global__ void __launch_bounds__(128) lin_combine_kernel(const __grid_constant_
 // dc / 32 slabs, a quarter of the arithmetic at da = dc = 128.
 constexpr int kLinRun = 32;
 
+constexpr int kLinMaxPasses = 3;
+struct LinSimtArgs {
+  LinPass p[kLinMaxPasses];  // passes of one launch (blockIdx.y), all with the same da
+};
+
 template <int DA>
 struct LinSmem {
   float a[kLinRun][DA + 4], b[kLinRun][DA + 4];
@@ -135,12 +140,14 @@ struct LinSmem {
 
 // OUT: write outputs from the entering state; otherwise the segment's own state.
 template <int DA, typename T, bool OUT>
-__global__ void __launch_bounds__(256) lin_simt_kernel(LinPass p) {
+__global__ void __launch_bounds__(256) lin_simt_kernel(const __grid_constant__ LinSimtArgs args) {
+  const LinPass p = args.p[blockIdx.y];
   extern __shared__ __align__(16) uint8_t lin_sm[];
   LinSmem<DA>& sm = *reinterpret_cast<LinSmem<DA>*>(lin_sm);
   const int tid = threadIdx.x;
   const int slabs = p.dc >> 5;
   int64_t x = blockIdx.x;
+  if (x >= (int64_t)p.B * p.H * p.nseg * slabs) return;  // passes of one launch may differ in dc
   const int slab = (int)(x % slabs);
   x /= slabs;
   const int j = (int)(x % p.nseg);

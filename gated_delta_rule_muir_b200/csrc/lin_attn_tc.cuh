@@ -51,8 +51,7 @@
 //   y_free    y1 and y2 read               (state -> MMA)
 //   cut       the parts in shared memory   (cut -> MMA)
 //   used3     third parts used             (MMA -> cut; without outputs)
-//   ds        dS in TMEM                   (MMA -> state, cut)
-//   ds_free   dS read                      (state -> MMA)
+//   ds, ds_free   dS in TMEM / read        (MMA -> state, cut / state -> MMA)
 //   s_ready   S for the next chunk in shared memory (state -> MMA)
 #pragma once
 
@@ -67,7 +66,6 @@ constexpr uint32_t kLtTile = 32768, kLtBox = 16384;  // 128 rows x 128 columns b
 constexpr int kLtSlots = 4;
 constexpr uint32_t kLtSmem = 7 * kLtTile + 1024;
 
-constexpr int kLinMaxPasses = 3;
 struct LinTcArgs {
   CUtensorMap a[kLinMaxPasses], b[kLinMaxPasses], c[kLinMaxPasses];  // boxes of 64 channels x 128 tokens
   CUtensorMap o[kLinMaxPasses];  // outputs, 64 x 32; unused for 32 channels
@@ -270,7 +268,11 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
   extern __shared__ __align__(1024) uint8_t lt_sm[];
   constexpr int SLOTS = kLtSlots;
   constexpr int TILES = OUT ? 3 : 2;  // per chunk: a, b, c or b, c
-  __shared__ uint64_t full[SLOTS], empty[SLOTS], b_scores, b_weights, b_y2, b_y, b_yfree, b_cut, b_used3, b_ds, b_dsfree, b_sready;
+  constexpr int CUTTERS = OUT ? 8 : 16;  // warps that cut b: without outputs the mask's warps too
+  // dS in one TMEM buffer, or in two in turn where the other accumulators leave room
+  auto ds_buf = [](int n) { return OUT ? 0 : n & 1; };
+  auto ds_phase = [](int n) { return (uint32_t)(OUT ? n : n >> 1) & 1u; };
+  __shared__ uint64_t full[SLOTS], empty[SLOTS], b_scores, b_weights, b_y2, b_y, b_yfree, b_cut, b_used3, b_ds[2], b_dsfree[2], b_sready;
   __shared__ uint32_t tslot;
   __shared__ float pw[kLtChunk];              // lambda^0 ..
   __shared__ __align__(16) float pcol[16];    // column factors of 16 columns (see the mask)
@@ -287,17 +289,19 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
   if (tid == 0) {
     for (int i = 0; i < SLOTS; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 9);
+      mbar_init(&empty[i], 1 + CUTTERS);
     }
     mbar_init(&b_scores, 1);
     mbar_init(&b_weights, 8);
     mbar_init(&b_y2, 1);
     mbar_init(&b_y, 1);
     mbar_init(&b_yfree, 8);
-    mbar_init(&b_cut, 8);
+    mbar_init(&b_cut, CUTTERS);
     mbar_init(&b_used3, 1);
-    mbar_init(&b_ds, 1);
-    mbar_init(&b_dsfree, 8);
+    mbar_init(&b_ds[0], 1);
+    mbar_init(&b_ds[1], 1);
+    mbar_init(&b_dsfree[0], 8);
+    mbar_init(&b_dsfree[1], 8);
     mbar_init(&b_sready, 8);
   }
   if (warp == 0) tmem_alloc(&tslot, 512);
@@ -307,7 +311,8 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tslot;
-  const uint32_t t_scores = tmem, t_y1 = tmem + 128, t_y2 = tmem + 256, t_ds = tmem + 384;
+  const uint32_t t_scores = tmem, t_y1 = tmem + 128, t_y2 = tmem + 256;
+  auto t_ds = [&](int n) { return tmem + 384u - 128u * (uint32_t)ds_buf(n); };
   // chunk n of the walk: its place in the segment
   auto chunk_at = [&](int n) { return p.reverse ? u.chunks - 1 - n : n; };
 
@@ -345,7 +350,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
     // from inside a one-lane branch, each product took three to four times as long.
     const int chunks = (int)__reduce_max_sync(0xffffffffu, (unsigned)u.chunks);
     const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
-    const uint32_t m_scores = tm, m_y1 = tm + 128, m_y2 = tm + 256, m_ds = tm + 384;
+    const uint32_t m_scores = tm, m_y1 = tm + 128, m_y2 = tm + 256;
     if (elect_one()) {
     bool ok = true;
     const uint32_t id_scores = idesc_bf16(128, 128, 0, 0), id_y = idesc_bf16(128, p.dc, 0, 1),
@@ -367,9 +372,10 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
     for (int n = 0; n < chunks && ok; ++n) {
       const uint32_t ph = (uint32_t)n & 1u;
       const int mb = n * TILES, ma = mb + 1, mc = mb + TILES - 1;
-      const uint32_t bt = slot(mb), ct = slot(mc);
+      const uint32_t bt = slot(mb), ct = slot(mc), m_ds = tm + 384u - 128u * (uint32_t)ds_buf(n);
       // c's tile: landed, and its rows past the last token cleared by the cutters
-      ok = landed(mc) && lane_wait(&b_cut, ph) && (n == 0 || lane_wait(&b_dsfree, ph ^ 1u));
+      ok = landed(mc) && lane_wait(&b_cut, ph) && 
+           (n <= ds_buf(1) || lane_wait(&b_dsfree[ds_buf(n)], ds_phase(n) ^ 1u));
       if (!ok) break;
       tc_fence_after();
       {
@@ -381,7 +387,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
           lt_product<8, false, true, true>(m_ds, part2(n, bt), ct, id_ds);
         }
         lt_product<8, true, true, true>(m_ds, part1(n, bt), ct, id_ds);
-        mma_commit(&b_ds);
+        mma_commit(&b_ds[ds_buf(n)]);
         if (PARTS == 3) mma_commit(&empty[mb % SLOTS]);
         if (!OUT) mma_commit(&empty[mc % SLOTS]);
       }
@@ -415,17 +421,17 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
     // are waited for here, or after a wait that ran out one more commit is
     if (ok) {
       if (chunks > 0) {
-        lane_wait(&b_ds, (uint32_t)(chunks - 1) & 1u);
+        lane_wait(&b_ds[ds_buf(chunks - 1)], ds_phase(chunks - 1));
         if (OUT) lane_wait(&b_y, (uint32_t)(chunks - 1) & 1u);
       }
     } else {
-      mma_commit(&b_ds);
-      mbar_wait_for(&b_ds, 0u, 1000000ull);
-      mbar_wait_for(&b_ds, 1u, 1000000ull);
+      mma_commit(&b_scores);
+      mbar_wait_for(&b_scores, 0u, 1000000ull);
+      mbar_wait_for(&b_scores, 1u, 1000000ull);
     }
     }
     }
-  } else if (warp < 12) {
+  } else if (OUT && warp < 12) {
     // ---- mask: thread = token row i of the chunk, every other 16 columns -------------------------
     regs_dec<56>();
     if constexpr (OUT) {
@@ -490,10 +496,11 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
   } else if (warp < 20) {
     // ---- cut b: thread = half a token row --------------------------------------------------------
     regs_dec<64>();
-    const int half = (warp - 12) >> 2;     // columns 64 half ..
+    constexpr int PIECES = OUT ? 8 : 4;                 // 8-column pieces of the row per thread
+    const int q0 = ((warp - (OUT ? 12 : 4)) >> 2) * PIECES;  // first of them
     const int r = (warp & 3) * 32 + lane;  // token row
-    const int bcols = p.da - 64 * half < 64 ? p.da - 64 * half : 64;  // at most 0: none
-    const uint32_t place = (uint32_t)half * kLtBox + (uint32_t)r * 128u;
+    const uint32_t place = (uint32_t)(q0 >> 3) * kLtBox + (uint32_t)r * 128u;
+    const int k0 = q0 & 7;  // in the box's row
     bool ok = true;
     for (int n = 0; n < u.chunks && ok; ++n) {
       const int64_t r0 = (int64_t)chunk_at(n) * kLtChunk;
@@ -505,16 +512,16 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       ok = warp_wait(&full[mb % SLOTS], (uint32_t)(mb / SLOTS) & 1u);
       if (L < kLtChunk) ok = ok && warp_wait(&full[mc % SLOTS], (uint32_t)(mc / SLOTS) & 1u);
       // the tiles of the last parts have been used; before third parts go over b, the scores have been formed
-      if (n > 0) ok = ok && warp_wait(OUT ? &b_ds : &b_used3, (uint32_t)(n - 1) & 1u);
+      if (n > 0) ok = ok && warp_wait(OUT ? &b_ds[0] : &b_used3, (uint32_t)(n - 1) & 1u);
       if (OUT && PARTS == 3) ok = ok && warp_wait(&b_scores, (uint32_t)n & 1u);
       if (!ok) break;
       // packed bf16, two parts: with the weight as w1 + w2, p1 = b w1 rounded, and
       // p2 = (b w1 - p1) + b w2, the bracket exact, rounded once
       const __nv_bfloat16 w1 = __float2bfloat16_rn(wt), w2 = __float2bfloat16_rn(wt - __bfloat162float(w1));
       const __nv_bfloat162 w11 = __halves2bfloat162(w1, w1), w22 = __halves2bfloat162(w2, w2);
-      if (bcols > 0) {
+      if (8 * q0 < p.da) {
 #pragma unroll 2
-        for (int c = 0; c < 8; ++c) {
+        for (int c = k0; c < k0 + PIECES; ++c) {
           const uint32_t at = (uint32_t)((c ^ (r & 7)) << 4);
           uint4 v = *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(line + at));
           if (r >= L) v = make_uint4(0u, 0u, 0u, 0u);  // past the last token: zeros, whatever they hold
@@ -551,8 +558,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       }
       if (r >= L) {  // c's rows past the last token: zero times anything must stay zero
         const uint32_t cline = base + (uint32_t)(mc % SLOTS) * kLtTile + place;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) sts128(cline + (uint32_t)(c << 4), make_uint4(0u, 0u, 0u, 0u));
+        for (int c = k0; c < k0 + PIECES; ++c) sts128(cline + (uint32_t)((c ^ (r & 7)) << 4), make_uint4(0u, 0u, 0u, 0u));
       }
       fence_async_smem();
       __syncwarp();
@@ -564,7 +570,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
     }
   } else {
     // ---- the state and outputs: thread = row r, columns 64 half .. -----------------------------------
-    regs_inc<112>();
+    regs_inc<OUT ? 112 : 104>();
     const int half = (warp - 20) >> 2;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t row = tmem_lane_base(warp);
@@ -674,14 +680,14 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
         const int64_t r0 = (int64_t)chunk_at(n - 1) * kLtChunk;
         const int L = (int)(u.valid - r0 < kLtChunk ? u.valid - r0 : kLtChunk);
         const LinDecay wl = lin_decay(u.c2, L);
-        ok = warp_wait(&b_ds, (uint32_t)(n - 1) & 1u);
+        ok = warp_wait(&b_ds[ds_buf(n - 1)], ds_phase(n - 1));
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if (64 * half + 16 * q < p.dc) {  // whole warps
             float d[16];
-            tmem_ld16(t_ds + row + (uint32_t)(64 * half + 16 * q), d);
+            tmem_ld16(t_ds(n - 1) + row + (uint32_t)(64 * half + 16 * q), d);
             const float2 g = make_float2(wl.g, wl.g), e = make_float2(wl.e, wl.e);
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
@@ -695,7 +701,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive1(&b_dsfree);
+        if (lane == 0) mbar_arrive1(&b_dsfree[ds_buf(n - 1)]);
       }
       if constexpr (OUT) {
         if (n < u.chunks) {
