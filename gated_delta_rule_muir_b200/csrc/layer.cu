@@ -504,12 +504,21 @@ int w4_validate(const char* who, int32_t K, int32_t O, int32_t group) {
   return MUIR_OK;
 }
 
+template <typename X, typename Y, int NB, int RT>
+void w4_launch(const muir::W4Params& p, int group, cudaStream_t s) {
+  const int tiles = (p.O + 15) / 16;
+  const dim3 grid((unsigned)((tiles + RT - 1) / RT), (unsigned)((p.n + 8 * NB - 1) / (8 * NB)));
+  if (group == 32) muir::w4_matvec_kernel<X, Y, NB, 4, RT><<<grid, 32 * muir::kW4Warps, 0, s>>>(p);
+  else if (group == 64) muir::w4_matvec_kernel<X, Y, NB, 2, RT><<<grid, 32 * muir::kW4Warps, 0, s>>>(p);
+  else muir::w4_matvec_kernel<X, Y, NB, 1, RT><<<grid, 32 * muir::kW4Warps, 0, s>>>(p);
+}
+// Four tiles of outputs per CTA once that still makes four CTAs for each SM: then x
+// is converted a quarter as often (50257 x 2048, eight e4m3 rows: 24 -> W4_WIDE us);
+// with fewer outputs one tile each, for more CTAs (6144 x 2048, one row: see there).
 template <typename X, typename Y, int NB>
 void w4_go(const muir::W4Params& p, int group, cudaStream_t s) {
-  const dim3 grid((unsigned)((p.O + 15) / 16), (unsigned)((p.n + 8 * NB - 1) / (8 * NB)));
-  if (group == 32) muir::w4_matvec_kernel<X, Y, NB, 4><<<grid, 32 * muir::kW4Warps, 0, s>>>(p);
-  else if (group == 64) muir::w4_matvec_kernel<X, Y, NB, 2><<<grid, 32 * muir::kW4Warps, 0, s>>>(p);
-  else muir::w4_matvec_kernel<X, Y, NB, 1><<<grid, 32 * muir::kW4Warps, 0, s>>>(p);
+  if (NB <= 2 && (p.O + 15) / 16 >= 16 * kSMs) w4_launch<X, Y, NB, NB <= 2 ? 2 : 1>(p, group, s);
+  else w4_launch<X, Y, NB, 1>(p, group, s);
 }
 template <typename X, typename Y>
 void w4_rows(const muir::W4Params& p, int group, cudaStream_t s) {

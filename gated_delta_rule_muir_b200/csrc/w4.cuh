@@ -14,9 +14,10 @@
 // can be summed by themselves and scaled once. Scales (bf16): [tile][block of 128
 // inputs][group in the block][16 outputs]. Outputs past O hold code 8 and scale 0.
 //
-// Codes become bf16 numbers exactly (128 + code is the bit pattern 0x4300 | code);
-// bf16 and e4m3 rows are exact in bf16 too, and fp32 rows are
-// cut into three bf16 parts whose sum has all 24 bits. The matrix instruction
+// Codes become numbers exactly (128 + code is the bf16 pattern 0x4300 | code, 1024 +
+// code the fp16 pattern 0x6400 | code). Products of bf16 rows are bf16, of e4m3 rows
+// fp16 (both exact, and one instruction converts a pair of e4m3 numbers), and fp32
+// rows are cut into three bf16 parts whose sum has all 24 bits. The matrix instruction
 // (mma.sync: eight columns are enough, and the weights come out of registers, not
 // shared memory) accumulates in fp32 within a group; the scaled sums are fp32.
 #pragma once
@@ -37,34 +38,57 @@ struct W4Params {
   int K, O;
 };
 
+template <bool HALF>
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  if constexpr (HALF)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Nibbles i and i + 4 of a word as two bf16 numbers (code - 8) 2^-10, exactly
-// ((128 + code) 2^-10 - 136 2^-10): a group's sum of up to 128 products then stays
-// below its largest input, so that no input overflows before its scale is applied.
+// The eight nibbles of a word as four pairs (nibbles i and i + 4) of numbers
+// (code - 8) 2^-10, exactly: the code beside a constant's exponent, less 8 and the
+// constant. A group's sum of up to 128 products then stays below its largest input,
+// so that no input overflows before its scale is applied. fp16 has room for a code
+// in bits 4 .. 7 as well (1024 + 16 code), which saves two of three shifts.
 constexpr float kW4Up = 1024.f;
-__device__ __forceinline__ uint32_t w4_pair(uint32_t w, int i) {
-  const uint32_t u = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-  const uint32_t m = 0x3A803A80u, c = 0xBE08BE08u;  // 2^-10, -136 2^-10
-  const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u), *reinterpret_cast<const __nv_bfloat162*>(&m),
-                                   *reinterpret_cast<const __nv_bfloat162*>(&c));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&r);
+template <bool HALF>
+__device__ __forceinline__ void w4_pairs(uint32_t w, uint32_t (&o)[4]) {
+  if constexpr (HALF) {
+    const auto number = [](uint32_t u, uint32_t m, uint32_t c) {
+      const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&u), *reinterpret_cast<const __half2*>(&m),
+                                *reinterpret_cast<const __half2*>(&c));
+      return *reinterpret_cast<const uint32_t*>(&r);
+    };
+    const uint32_t v = w >> 8;
+    o[0] = number((w & 0x000F000Fu) | 0x64006400u, 0x14001400u, 0xBC08BC08u);  // 2^-10, -1032 2^-10
+    o[1] = number((w & 0x00F000F0u) | 0x64006400u, 0x04000400u, 0xAC80AC80u);  // 2^-14, -(1024 + 128) 2^-14
+    o[2] = number((v & 0x000F000Fu) | 0x64006400u, 0x14001400u, 0xBC08BC08u);
+    o[3] = number((v & 0x00F000F0u) | 0x64006400u, 0x04000400u, 0xAC80AC80u);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+      const uint32_t m = 0x3A803A80u, c = 0xBE08BE08u;  // 2^-10, -136 2^-10
+      const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&u),
+                                       *reinterpret_cast<const __nv_bfloat162*>(&m),
+                                       *reinterpret_cast<const __nv_bfloat162*>(&c));
+      o[i] = *reinterpret_cast<const uint32_t*>(&r);
+    }
+  }
 }
 
 // 8 consecutive inputs of one row as matrix operands: part p, pairs (0,4), (1,5), (2,6), (3,7).
 template <typename X> struct W4X;
 template <> struct W4X<__nv_bfloat16> {
   static constexpr int PARTS = 1;
+  static constexpr bool HALF = false;
   static __device__ __forceinline__ void get(const __nv_bfloat16* p, uint32_t (&o)[1][4]) {
     const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
     o[0][0] = __byte_perm(u.x, u.z, 0x5410);
@@ -75,19 +99,20 @@ template <> struct W4X<__nv_bfloat16> {
 };
 template <> struct W4X<__nv_fp8_e4m3> {
   static constexpr int PARTS = 1;
+  static constexpr bool HALF = true;
   static __device__ __forceinline__ void get(const __nv_fp8_e4m3* p, uint32_t (&o)[1][4]) {
     const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {  // elements i (of u.x) and i + 4 (of u.y)
-      const uint32_t two = ((u.x >> (8 * i)) & 0xFFu) | (((u.y >> (8 * i)) & 0xFFu) << 8);
+      const uint32_t two = __byte_perm(u.x, u.y, i | ((i + 4) << 4));
       const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      o[0][i] = pack_bf16(f.x, f.y);
+      o[0][i] = *reinterpret_cast<const uint32_t*>(&h);
     }
   }
 };
 template <> struct W4X<float> {
   static constexpr int PARTS = 3;
+  static constexpr bool HALF = false;
   static __device__ __forceinline__ void get(const float* p, uint32_t (&o)[3][4]) {
     float f[8];
     Elt<float>::ld8(p, f);
@@ -104,85 +129,130 @@ template <> struct W4X<float> {
   }
 };
 
-constexpr int kW4Warps = 8;
+constexpr int kW4Warps = 4;
 
-// One CTA per tile of 16 outputs and 8 NB rows of x; the warps share the inputs.
-// GPB: groups per block of 128 inputs (1, 2 or 4).
-template <typename X, typename Y, int NB, int GPB>
-__global__ void __launch_bounds__(32 * kW4Warps) w4_matvec_kernel(W4Params p) {
+// One CTA per RT tiles of 16 outputs and 8 NB rows of x; the warps share the inputs,
+// so each piece of x is fetched and converted once per RT tiles. GPB: groups per
+// block of 128 inputs (1, 2 or 4).
+template <typename X, typename Y, int NB, int GPB, int RT>
+__global__ void __launch_bounds__(32 * kW4Warps, NB == 1 ? 6 : 3) w4_matvec_kernel(W4Params p) {
+  using XL = W4X<X>;
   __shared__ float red[kW4Warps][NB][32][4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int blocks = p.K >> 7;
-  const int64_t tile = blockIdx.x;
+  const int64_t tiles = (p.O + 15) >> 4, tile0 = (int64_t)blockIdx.x * RT;
   const int64_t n0 = (int64_t)blockIdx.y * (8 * NB);
   const X* x = static_cast<const X*>(p.x);
-  float acc[NB][4];
+  float acc[RT][NB][4];
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
+  for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[b][i] = 0.f;
-  const uint4* wt = reinterpret_cast<const uint4*>(p.wq + tile * blocks * 1024) + lane * 2;
-  const __nv_bfloat16* st = p.ws + tile * blocks * (GPB * 16) + g;
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[rt][b][i] = 0.f;
+  // this lane's first weights, scales and inputs; a block of inputs further on each turn
+  const uint4* wt[RT];
+  const __nv_bfloat16* st[RT];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    // tiles past the last repeat it; their sums are not stored
+    const int64_t at = (tile0 + rt < tiles ? tile0 + rt : tiles - 1) * blocks + warp;
+    wt[rt] = reinterpret_cast<const uint4*>(p.wq + at * 1024) + lane * 2;
+    st[rt] = p.ws + at * (GPB * 16) + g;
+  }
+  const X* xt[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) xt[b] = x + (n0 + 8 * b + g) * p.K + warp * 128 + 8 * t;
   for (int kb = warp; kb < blocks; kb += kW4Warps) {
-    const uint4 lo = __ldg(wt + (int64_t)kb * 64), hi = __ldg(wt + (int64_t)kb * 64 + 1);
-    const uint32_t w0[4] = {lo.x, lo.y, lo.z, lo.w}, w1[4] = {hi.x, hi.y, hi.z, hi.w};
+    uint4 w[RT][2];
+    __nv_bfloat16 sc[RT][GPB][2];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      w[rt][0] = __ldg(wt[rt]);
+      w[rt][1] = __ldg(wt[rt] + 1);
+      wt[rt] += 64 * kW4Warps;
+#pragma unroll
+      for (int gr = 0; gr < GPB; ++gr) {
+        sc[rt][gr][0] = __ldg(st[rt] + gr * 16);
+        sc[rt][gr][1] = __ldg(st[rt] + gr * 16 + 8);
+      }
+      st[rt] += GPB * 16 * kW4Warps;
+    }
 #pragma unroll
     for (int gr = 0; gr < GPB; ++gr) {
-      float part[NB][4];
+      float part[RT][NB][4];
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+      for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) part[b][i] = 0.f;
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) part[rt][b][i] = 0.f;
 #pragma unroll
       for (int jj = 0; jj < 4 / GPB; ++jj) {
         const int j = gr * (4 / GPB) + jj;
-        const uint32_t a0[4] = {w4_pair(w0[j], 0), w4_pair(w1[j], 0), w4_pair(w0[j], 1), w4_pair(w1[j], 1)};
-        const uint32_t a1[4] = {w4_pair(w0[j], 2), w4_pair(w1[j], 2), w4_pair(w0[j], 3), w4_pair(w1[j], 3)};
+        uint32_t xb[NB][XL::PARTS][4];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          uint32_t xb[W4X<X>::PARTS][4];
           const int64_t r = n0 + 8 * b + g;
           if (r < p.n) {
-            W4X<X>::get(x + r * p.K + kb * 128 + 32 * j + 8 * t, xb);
+            XL::get(xt[b] + 32 * j, xb[b]);
           } else {
 #pragma unroll
-            for (int m = 0; m < W4X<X>::PARTS; ++m)
+            for (int m = 0; m < XL::PARTS; ++m)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) xb[m][i] = 0u;
-          }
-#pragma unroll
-          for (int m = 0; m < W4X<X>::PARTS; ++m) {
-            mma_16816(part[b], a0, xb[m][0], xb[m][1]);
-            mma_16816(part[b], a1, xb[m][2], xb[m][3]);
+              for (int i = 0; i < 4; ++i) xb[b][m][i] = 0u;
           }
         }
-      }
-      const float s0 = kW4Up * __bfloat162float(__ldg(st + (int64_t)kb * (GPB * 16) + gr * 16));
-      const float s1 = kW4Up * __bfloat162float(__ldg(st + (int64_t)kb * (GPB * 16) + gr * 16 + 8));
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        acc[b][0] = fmaf(s0, part[b][0], acc[b][0]);
-        acc[b][1] = fmaf(s0, part[b][1], acc[b][1]);
-        acc[b][2] = fmaf(s1, part[b][2], acc[b][2]);
-        acc[b][3] = fmaf(s1, part[b][3], acc[b][3]);
+        for (int rt = 0; rt < RT; ++rt) {
+          const uint32_t u0 = reinterpret_cast<const uint32_t*>(&w[rt][0])[j], u1 = reinterpret_cast<const uint32_t*>(&w[rt][1])[j];
+          uint32_t n0[4], n1[4];
+          w4_pairs<XL::HALF>(u0, n0);
+          w4_pairs<XL::HALF>(u1, n1);
+          const uint32_t a0[4] = {n0[0], n1[0], n0[1], n1[1]}, a1[4] = {n0[2], n1[2], n0[3], n1[3]};
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int m = 0; m < XL::PARTS; ++m) {
+              mma_16816<XL::HALF>(part[rt][b], a0, xb[b][m][0], xb[b][m][1]);
+              mma_16816<XL::HALF>(part[rt][b], a1, xb[b][m][2], xb[b][m][3]);
+            }
+        }
+      }
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const float s0 = kW4Up * __bfloat162float(sc[rt][gr][0]), s1 = kW4Up * __bfloat162float(sc[rt][gr][1]);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          acc[rt][b][0] = fmaf(s0, part[rt][b][0], acc[rt][b][0]);
+          acc[rt][b][1] = fmaf(s0, part[rt][b][1], acc[rt][b][1]);
+          acc[rt][b][2] = fmaf(s1, part[rt][b][2], acc[rt][b][2]);
+          acc[rt][b][3] = fmaf(s1, part[rt][b][3], acc[rt][b][3]);
+        }
       }
     }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) xt[b] += 128 * kW4Warps;
   }
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
-    *reinterpret_cast<float4*>(red[warp][b][lane]) = make_float4(acc[b][0], acc[b][1], acc[b][2], acc[b][3]);
-  __syncthreads();
-  // 16 outputs x 8 NB rows; output o of row r is element (o / 8) * 2 + r % 2 of lane (o % 8) * 4 + (r % 8) / 2
-  for (int i = threadIdx.x; i < 128 * NB; i += 32 * kW4Warps) {
-    const int o = i & 15, r = i >> 4;
-    const int l = (o & 7) * 4 + ((r & 7) >> 1), e = (o >> 3) * 2 + (r & 1);
-    float s = 0.f;
+  for (int rt = 0; rt < RT; ++rt) {
+    if (rt > 0) __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kW4Warps; ++w) s += red[w][r >> 3][l][e];
-    const int64_t row = n0 + r, col = tile * 16 + o;
-    if (row < p.n && col < p.O) {
-      if (p.x_scale) s *= __ldg(p.x_scale + row);
-      Elt<Y>::st(static_cast<Y*>(p.y) + row * p.O + col, s);
+    for (int b = 0; b < NB; ++b)
+      *reinterpret_cast<float4*>(red[warp][b][lane]) = make_float4(acc[rt][b][0], acc[rt][b][1], acc[rt][b][2], acc[rt][b][3]);
+    __syncthreads();
+    // 16 outputs x 8 NB rows; output o of row r is element (o / 8) * 2 + r % 2 of lane (o % 8) * 4 + (r % 8) / 2
+    for (int i = threadIdx.x; i < 128 * NB; i += 32 * kW4Warps) {
+      const int o = i & 15, r = i >> 4;
+      const int l = (o & 7) * 4 + ((r & 7) >> 1), e = (o >> 3) * 2 + (r & 1);
+      float s = 0.f;
+#pragma unroll
+      for (int k = 0; k < kW4Warps; ++k) s += red[k][r >> 3][l][e];
+      const int64_t row = n0 + r, col = (tile0 + rt) * 16 + o;
+      if (row < p.n && col < p.O) {
+        if (p.x_scale) s *= __ldg(p.x_scale + row);
+        Elt<Y>::st(static_cast<Y*>(p.y) + row * p.O + col, s);
+      }
     }
   }
 }
