@@ -487,7 +487,7 @@ int muir_rms_norm_bwd(const void* dy, const void* h, const float* weight, const 
   }
   if ((rc = check_launch("rms_norm_bwd"))) return rc;
   LaunchScope l("rms_norm_dw", s);
-  muir::rms_norm_dw_kernel<<<(unsigned)((d + 31) / 32), 256, 0, s>>>(p.part, dweight, (int)blocks, d);
+  muir::rms_norm_dw_kernel<<<(unsigned)((d + 31) / 32), 1024, 0, s>>>(p.part, dweight, (int)blocks, d);
   return check_launch("rms_norm_dw");
 }
 

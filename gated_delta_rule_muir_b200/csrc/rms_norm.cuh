@@ -159,7 +159,7 @@ struct NormBwdParams {
 // dweight in registers; the partial sums go to the workspace and are added in a
 // fixed order by rms_norm_dw_kernel, so that a repeated call gives the same bits.
 template <typename T, int NT, int V>
-__global__ void __launch_bounds__(NT) rms_norm_bwd_kernel(NormBwdParams p) {
+__global__ void __launch_bounds__(NT, NT <= 512 ? 1024 / NT : 1) rms_norm_bwd_kernel(NormBwdParams p) {
   __shared__ float slot[2][32];
   const int lane = threadIdx.x;
   float dw[V][8], w[V][8];
@@ -170,18 +170,37 @@ __global__ void __launch_bounds__(NT) rms_norm_bwd_kernel(NormBwdParams p) {
     for (int i = 0; i < 8; ++i) { dw[v][i] = 0.f; w[v][i] = 0.f; }
     if (e < p.d) Elt<float>::ld8(p.weight + e, w[v]);
   }
+  // the next row is on its way while this one is reduced
+  Pack8<T> nh[V], ng[V], nr[V];
+  float nrstd = 0.f;
+  auto fetch = [&](int64_t row) {
+    if (row >= p.n) return;
+    nrstd = __ldg(p.rstd + row);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = (v * NT + lane) * 8;
+      if (e < p.d) {
+        nh[v].ld(static_cast<const T*>(p.h) + row * p.d + e);
+        ng[v].ld(static_cast<const T*>(p.dy) + row * p.d + e);
+        if (p.dh) nr[v].ld(static_cast<const T*>(p.dh) + row * p.d + e);
+      }
+    }
+  };
+  fetch(blockIdx.x);
   int turn = 0;
   for (int64_t row = blockIdx.x; row < p.n; row += gridDim.x, turn ^= 1) {
     const int64_t off = row * p.d;
-    const float rstd = __ldg(p.rstd + row);
+    const float rstd = nrstd;
     float xh[V][8], g[V][8];
+    Pack8<T> r[V];
     float dot = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int e = (v * NT + lane) * 8;
       if (e < p.d) {
-        Elt<T>::ld8(static_cast<const T*>(p.h) + off + e, xh[v]);
-        Elt<T>::ld8(static_cast<const T*>(p.dy) + off + e, g[v]);
+        nh[v].get(xh[v]);
+        ng[v].get(g[v]);
+        r[v] = nr[v];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           xh[v][i] *= rstd;
@@ -191,6 +210,7 @@ __global__ void __launch_bounds__(NT) rms_norm_bwd_kernel(NormBwdParams p) {
         }
       }
     }
+    fetch(row + gridDim.x);
     dot = row_sum<NT>(dot, slot[turn]) / (float)p.d;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -200,10 +220,10 @@ __global__ void __launch_bounds__(NT) rms_norm_bwd_kernel(NormBwdParams p) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) o[i] = rstd * fmaf(-xh[v][i], dot, g[v][i]);
         if (p.dh) {
-          float r[8];
-          Elt<T>::ld8(static_cast<const T*>(p.dh) + off + e, r);
+          float x[8];
+          r[v].get(x);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] += r[i];
+          for (int i = 0; i < 8; ++i) o[i] += x[i];
         }
         Elt<T>::st8(static_cast<T*>(p.dx) + off + e, o);
       }
@@ -216,21 +236,21 @@ __global__ void __launch_bounds__(NT) rms_norm_bwd_kernel(NormBwdParams p) {
   }
 }
 
-// dweight = the column sums of part [m][d]: 32 columns per CTA, 32 x 8 threads.
-__global__ void __launch_bounds__(256) rms_norm_dw_kernel(const float* __restrict__ part, float* __restrict__ dweight, int m,
-                                                          int d) {
-  __shared__ float s[8][33];
+// dweight = the column sums of part [m][d]: 32 columns per CTA, 32 x 32 threads, each
+// thread's rows and then the threads' sums in a fixed order.
+__global__ void __launch_bounds__(1024) rms_norm_dw_kernel(const float* __restrict__ part, float* __restrict__ dweight, int m,
+                                                           int d) {
+  __shared__ float s[32][33];
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5;
   float a = 0.f;
-  if (c < d)
-    for (int i = r; i < m; i += 8) a += part[(int64_t)i * d + c];
-  s[r][threadIdx.x & 31] = a;
-  __syncthreads();
-  if (r == 0 && c < d) {
-#pragma unroll
-    for (int i = 1; i < 8; ++i) a += s[i][threadIdx.x];
-    dweight[c] = a;
+  if (c < d) {
+#pragma unroll 8
+    for (int i = r; i < m; i += 32) a += part[(int64_t)i * d + c];
   }
+  s[threadIdx.x & 31][r] = a;
+  __syncthreads();
+  a = warp_sum(s[r][threadIdx.x & 31]);  // warp r: column r of the CTA
+  if ((threadIdx.x & 31) == 0 && blockIdx.x * 32 + r < (unsigned)d) dweight[blockIdx.x * 32 + r] = a;
 }
 
 }  // namespace muir
