@@ -439,9 +439,9 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
     const uint32_t row = tmem_lane_base(warp);
     // 16 columns at a time in one short loop (an unrolled body of this size runs at the
     // pace of instruction fetches). lambda^gap = (row factor) (column factor), the
-    // column factor at most 1 and the row factor at most lambda^-15: below 2^-8 that
-    // could overflow, and the powers are formed one by one.
-    const bool mild = u.c2 > -8.f;
+    // column factor at most 1 and the row factor at most lambda^-15, 2^60 for decays
+    // above 2^-4; below that the powers are taken from the table one by one.
+    const bool mild = u.c2 > -4.f;
     bool ok = true;
     for (int n = 0; n < u.chunks && ok; ++n) {
       const uint32_t ph = (uint32_t)n & 1u;
@@ -463,27 +463,29 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
           float v[16];
           tmem_ld16(t_scores + row + (uint32_t)c, v);
           const int e = p.reverse ? c - i : i - c - 15;
-          if (__any_sync(0xffffffffu, lo > 0 || hi < 16)) {
-            // dropped, not multiplied by zero: a score that does not count may be anything
+          if (mild) {
+            const float rf = p.p_scale * exp2f(u.c2 * (float)max(e, -15));
 #pragma unroll
-            for (int s = 0; s < 16; ++s) v[s] = (s >= lo) & (s < hi) ? v[s] : 0.f;
-          }
-          if (!mild) {
+            for (int q = 0; q < 4; ++q) {
+              const float4 cf = *reinterpret_cast<const float4*>(&pcol[4 * q]);
+              const float2 f = __fmul2_rn(make_float2(v[4 * q], v[4 * q + 1]), __fmul2_rn(make_float2(cf.x, cf.y), make_float2(rf, rf)));
+              const float2 g = __fmul2_rn(make_float2(v[4 * q + 2], v[4 * q + 3]), __fmul2_rn(make_float2(cf.z, cf.w), make_float2(rf, rf)));
+              v[4 * q] = f.x;
+              v[4 * q + 1] = f.y;
+              v[4 * q + 2] = g.x;
+              v[4 * q + 3] = g.y;
+            }
+          } else {
 #pragma unroll
             for (int s = 0; s < 16; ++s) v[s] *= p.p_scale * pw[max(0, p.reverse ? e + s : e + 15 - s)];
           }
-          const float rf = p.p_scale * exp2f(u.c2 * (float)max(e, -15));
+          if (__any_sync(0xffffffffu, lo > 0 || hi < 16)) {
+            // dropped, not multiplied by zero: what does not count may be anything
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float4 cf = *reinterpret_cast<const float4*>(&pcol[4 * q]);
-            float2 f = make_float2(v[4 * q], v[4 * q + 1]), g = make_float2(v[4 * q + 2], v[4 * q + 3]);
-            if (mild) {
-              f = __fmul2_rn(f, __fmul2_rn(make_float2(cf.x, cf.y), make_float2(rf, rf)));
-              g = __fmul2_rn(g, __fmul2_rn(make_float2(cf.z, cf.w), make_float2(rf, rf)));
-            }
-            wd[2 * q] = bf16x2(f.x, f.y);
-            wd[2 * q + 1] = bf16x2(g.x, g.y);
+            for (int s = 0; s < 16; ++s) v[s] = (s >= lo) & (s < hi) ? v[s] : 0.f;
           }
+#pragma unroll
+          for (int q = 0; q < 8; ++q) wd[q] = bf16x2(v[2 * q], v[2 * q + 1]);
         }
         // over the first half of the scores they come from
         tmem_st8(t_scores + row + (uint32_t)c, wd);

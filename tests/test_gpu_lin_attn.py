@@ -101,6 +101,23 @@ def test_extreme_decays_and_scales(cuda_ok, dtype, state):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("scale", [1e9, -1e-9])
+def test_large_and_small_scales(cuda_ok, dtype, scale):
+    """Decays on both sides of each way of forming their powers."""
+    ld = [-2.7, -2.8, -5.5, -5.6, -0.001, -30.0]
+    d, t = _make(1, 200, len(ld), 64, 64, dtype, seed=9, log_decay=ld)
+    _run(d, t, dtype, None, scale, True)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("case", [(1, 400, 1, 32, 32), (1, 260, 1, 32, 128), (2, 260, 1, 64, 32), (40, 130, 4, 64, 64),
+                                  (1, 3000, 1, 128, 128)])
+def test_one_head_many_sequences_and_many_segments(cuda_ok, dtype, case):
+    d, t = _make(*case, dtype, seed=10)
+    _run(d, t, dtype, None, 1.0, False)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_no_tokens(cuda_ok, dtype):
     d, t = _make(2, 0, 2, 32, 64, dtype)
     y, S = muir.lin_attn_fwd(t["q"], t["k"], t["v"], t["ld"], S0=t["S0"])
@@ -201,6 +218,25 @@ def test_repeats_streams_and_graphs_agree(cuda_ok, dtype):
     torch.cuda.synchronize()
     for _, out in graphs:
         assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_dS0_keeps_its_own_buffer(cuda_ok):
+    d, t = _make(1, 64, 2, 64, 64, torch.bfloat16)
+    for n in ("S0", "dS_T"):
+        with pytest.raises(muir.MuirError, match="dS0"):
+            muir.lin_attn_bwd(t["q"], t["k"], t["v"], t["ld"], t["dy"], S0=t["S0"], dS_T=t["dS_T"], outputs={"dS0": t[n]})
+
+
+def test_outputs_at_other_alignments(cuda_ok):
+    """Buffers 16 bytes past a 32-byte boundary give the same bits."""
+    for dv in (32, 64):
+        d, t = _make(1, 200, 2, 64, dv, torch.bfloat16, seed=11)
+        y, S = muir.lin_attn_fwd(t["q"], t["k"], t["v"], t["ld"], S0=t["S0"])
+        y2 = torch.empty(y.numel() + 8, dtype=y.dtype, device="cuda")[8:].view(y.shape)
+        S2 = torch.empty(S.numel() + 4, device="cuda")[4:].view(S.shape)
+        assert y2.data_ptr() % 32 == 16 and S2.data_ptr() % 32 == 16
+        muir.lin_attn_fwd(t["q"], t["k"], t["v"], t["ld"], S0=t["S0"], y=y2, S_T=S2)
+        assert torch.equal(y, y2) and torch.equal(S, S2)
 
 
 def test_offsets_past_32_bits(cuda_ok):
