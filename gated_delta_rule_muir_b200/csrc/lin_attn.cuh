@@ -119,11 +119,13 @@ __global__ void __launch_bounds__(128) lin_combine_kernel(const __grid_constant_
 
 // ---- CUDA-core pass -----------------------------------------------------------
 //
-// One CTA of 256 threads per (b, h, segment, 32 columns of c), 32 tokens at a
-// time: the token-token products of the run in shared memory, the state's slab
-// [da][32] in shared memory in fp32. The products are recomputed by each of the
-// dc / 32 slabs, a quarter of the arithmetic at da = dc = 128.
-constexpr int kLinRun = 32;
+// One CTA of 256 threads per (b, h, segment, 32 columns of c), 64 tokens at a time:
+// the token-token products of the run and the state's slab [da][32] in shared memory
+// in fp32. The products are recomputed by each of the dc / 32 slabs, a third of the
+// arithmetic at da = dc = 128. Bound by shared-memory reads: the tiles (4 x 4 scores,
+// 2 x 4 outputs and da / 32 x 4 state elements per thread, all read four floats at a
+// time) take about seven products for each 16-byte read.
+constexpr int kLinRun = 64;
 
 constexpr int kLinMaxPasses = 3;
 struct LinSimtArgs {
@@ -133,10 +135,18 @@ struct LinSimtArgs {
 template <int DA>
 struct LinSmem {
   float a[kLinRun][DA + 4], b[kLinRun][DA + 4];
-  float c[kLinRun][36], p[kLinRun][36];
+  float c[kLinRun][36], p[kLinRun][kLinRun + 4];
   float s[DA][36];
   float pw[kLinRun + 2];  // lambda^0 ..
 };
+
+__device__ __forceinline__ float4 lds4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ void fma4(float (&d)[4], float a, const float4& b) {
+  d[0] = fmaf(a, b.x, d[0]);
+  d[1] = fmaf(a, b.y, d[1]);
+  d[2] = fmaf(a, b.z, d[2]);
+  d[3] = fmaf(a, b.w, d[3]);
+}
 
 // OUT: write outputs from the entering state; otherwise the segment's own state.
 template <int DA, typename T, bool OUT>
@@ -158,7 +168,7 @@ __global__ void __launch_bounds__(256) lin_simt_kernel(const __grid_constant__ L
   const float c2 = lin_log2(p.log_decay, h);
   const int col0 = slab * 32;
   const int nstate = DA * p.dc;
-  for (int i = tid; i < kLinRun + 2; i += 256) sm.pw[i] = exp2f(c2 * (float)i);
+  if (tid < kLinRun + 2) sm.pw[tid] = exp2f(c2 * (float)tid);
 
   // the entering state
   {
@@ -181,12 +191,14 @@ __global__ void __launch_bounds__(256) lin_simt_kernel(const __grid_constant__ L
     }
   }
 
+  const int tr = tid >> 3, cg = (tid & 7) * 4;  // token rows tr, tr + 32 (or state rows); first of 4 columns
   const int64_t runs = (valid + kLinRun - 1) / kLinRun;
   for (int64_t n = 0; n < runs; ++n) {
     const int64_t r0 = (p.reverse ? runs - 1 - n : n) * kLinRun;  // first token of the run, in the segment
     const int L = (int)(valid - r0 < kLinRun ? valid - r0 : kLinRun);
     const int64_t row = (int64_t)b * p.T + t0 + r0;
     __syncthreads();
+#pragma unroll 4
     for (int i = tid; i < kLinRun * (DA / 4); i += 256) {
       const int t = i / (DA / 4), c4 = (i % (DA / 4)) * 4;
       float va[4] = {0.f, 0.f, 0.f, 0.f}, vb[4] = {0.f, 0.f, 0.f, 0.f};
@@ -198,6 +210,7 @@ __global__ void __launch_bounds__(256) lin_simt_kernel(const __grid_constant__ L
       if constexpr (OUT) *reinterpret_cast<float4*>(&sm.a[t][c4]) = make_float4(va[0], va[1], va[2], va[3]);
       *reinterpret_cast<float4*>(&sm.b[t][c4]) = make_float4(vb[0], vb[1], vb[2], vb[3]);
     }
+#pragma unroll
     for (int i = tid; i < kLinRun * 8; i += 256) {
       const int t = i >> 3, c4 = (i & 7) * 4;
       float vc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -205,64 +218,89 @@ __global__ void __launch_bounds__(256) lin_simt_kernel(const __grid_constant__ L
       *reinterpret_cast<float4*>(&sm.c[t][c4]) = make_float4(vc[0], vc[1], vc[2], vc[3]);
     }
     __syncthreads();
-    const int tr = tid >> 3, cg = (tid & 7) * 4;  // token row, first of 4 columns
     if constexpr (OUT) {
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int k = 0; k < DA; k += 4) {
-        const float4 av = *reinterpret_cast<const float4*>(&sm.a[tr][k]);
+      {  // scores: rows ti + 16 m, columns si + 16 k
+        const int ti = tid >> 4, si = tid & 15;
+        float acc[4][4];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const float4 bv = *reinterpret_cast<const float4*>(&sm.b[(tid & 7) + 8 * m][k]);
-          acc[m] = fmaf(av.x, bv.x, fmaf(av.y, bv.y, fmaf(av.z, bv.z, fmaf(av.w, bv.w, acc[m]))));
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[m][k] = 0.f;
+#pragma unroll 2
+        for (int e = 0; e < DA; e += 4) {
+          float4 av[4], bv[4];
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            av[m] = lds4(&sm.a[ti + 16 * m][e]);
+            bv[m] = lds4(&sm.b[si + 16 * m][e]);
+          }
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              acc[m][k] = fmaf(av[m].x, bv[k].x,
+                               fmaf(av[m].y, bv[k].y, fmaf(av[m].z, bv[k].z, fmaf(av[m].w, bv[k].w, acc[m][k]))));
         }
-      }
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        const int s = (tid & 7) + 8 * m;
-        const int gap = p.reverse ? s - tr : tr - s;
-        // a masked pair is dropped, not multiplied by zero (rows past L hold zeros)
-        sm.p[tr][s] = gap >= 0 && s < L ? acc[m] * sm.pw[gap] * p.p_scale : 0.f;
+        for (int m = 0; m < 4; ++m)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int t = ti + 16 * m, s = si + 16 * k, gap = p.reverse ? s - t : t - s;
+            // a masked pair is dropped, not multiplied by zero (rows past L hold zeros)
+            sm.p[t][s] = gap >= 0 && s < L ? acc[m][k] * sm.pw[gap] * p.p_scale : 0.f;
+          }
       }
       __syncthreads();
-      float o[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int s = 0; s < kLinRun; ++s) {
-        const float pv = sm.p[tr][s];
-        const float4 cv = *reinterpret_cast<const float4*>(&sm.c[s][cg]);
-        o[0] = fmaf(pv, cv.x, o[0]); o[1] = fmaf(pv, cv.y, o[1]); o[2] = fmaf(pv, cv.z, o[2]); o[3] = fmaf(pv, cv.w, o[3]);
+      float o[2][4] = {}, u[2][4] = {};
+#pragma unroll 4
+      for (int s = 0; s < kLinRun; s += 4) {
+        const float4 p0 = lds4(&sm.p[tr][s]), p1 = lds4(&sm.p[tr + 32][s]);
+        const float4 c0 = lds4(&sm.c[s][cg]), c1 = lds4(&sm.c[s + 1][cg]), c2v = lds4(&sm.c[s + 2][cg]), c3 = lds4(&sm.c[s + 3][cg]);
+        fma4(o[0], p0.x, c0); fma4(o[0], p0.y, c1); fma4(o[0], p0.z, c2v); fma4(o[0], p0.w, c3);
+        fma4(o[1], p1.x, c0); fma4(o[1], p1.y, c1); fma4(o[1], p1.z, c2v); fma4(o[1], p1.w, c3);
       }
-      for (int k = 0; k < DA; ++k) {
-        const float av = sm.a[tr][k];
-        const float4 sv = *reinterpret_cast<const float4*>(&sm.s[k][cg]);
-        u[0] = fmaf(av, sv.x, u[0]); u[1] = fmaf(av, sv.y, u[1]); u[2] = fmaf(av, sv.z, u[2]); u[3] = fmaf(av, sv.w, u[3]);
+#pragma unroll 4
+      for (int e = 0; e < DA; e += 4) {
+        const float4 a0 = lds4(&sm.a[tr][e]), a1 = lds4(&sm.a[tr + 32][e]);
+        const float4 s0 = lds4(&sm.s[e][cg]), s1 = lds4(&sm.s[e + 1][cg]), s2 = lds4(&sm.s[e + 2][cg]), s3 = lds4(&sm.s[e + 3][cg]);
+        fma4(u[0], a0.x, s0); fma4(u[0], a0.y, s1); fma4(u[0], a0.z, s2); fma4(u[0], a0.w, s3);
+        fma4(u[1], a1.x, s0); fma4(u[1], a1.y, s1); fma4(u[1], a1.z, s2); fma4(u[1], a1.w, s3);
       }
-      if (tr < L) {
-        const float w = p.o_scale * sm.pw[p.reverse ? L - 1 - tr : tr + 1];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) o[m] = fmaf(w, u[m], o[m]);
-        Elt<T>::st4(static_cast<T*>(p.out) + ((row + tr) * p.H + h) * p.dc + col0 + cg, o);
+      for (int m = 0; m < 2; ++m) {
+        const int t = tr + 32 * m;
+        if (t < L) {
+          const float w = p.o_scale * sm.pw[p.reverse ? L - 1 - t : t + 1];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[m][i] = fmaf(w, u[m][i], o[m][i]);
+          Elt<T>::st4(static_cast<T*>(p.out) + ((row + t) * p.H + h) * p.dc + col0 + cg, o[m]);
+        }
       }
       __syncthreads();
     }
-    // S = lambda^L S + sum_s weight_s b_s c_s^T; rows tr, tr + 32, ..
-    float up[DA / 32][4];
-#pragma unroll
-    for (int m = 0; m < DA / 32; ++m)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) up[m][q] = 0.f;
+    // S = lambda^L S + sum_s weight_s b_s c_s^T: rows RPT tr .., columns cg ..
+    constexpr int RPT = DA / 32;
+    float up[RPT][4] = {};
+#pragma unroll 4
     for (int s = 0; s < L; ++s) {
       const float w = p.u_scale * sm.pw[p.reverse ? s + 1 : L - 1 - s];
-      const float4 cv = *reinterpret_cast<const float4*>(&sm.c[s][cg]);
+      float4 cv = lds4(&sm.c[s][cg]);
+      cv = make_float4(cv.x * w, cv.y * w, cv.z * w, cv.w * w);
+      float bv[RPT];
+      if constexpr (RPT == 4) {
+        const float4 t = lds4(&sm.b[s][4 * tr]);
+        bv[0] = t.x; bv[1] = t.y; bv[2] = t.z; bv[3] = t.w;
+      } else {
 #pragma unroll
-      for (int m = 0; m < DA / 32; ++m) {
-        const float bw = sm.b[s][tr + 32 * m] * w;
-        up[m][0] = fmaf(bw, cv.x, up[m][0]); up[m][1] = fmaf(bw, cv.y, up[m][1]);
-        up[m][2] = fmaf(bw, cv.z, up[m][2]); up[m][3] = fmaf(bw, cv.w, up[m][3]);
+        for (int m = 0; m < RPT; ++m) bv[m] = sm.b[s][RPT * tr + m];
       }
+#pragma unroll
+      for (int m = 0; m < RPT; ++m) fma4(up[m], bv[m], cv);
     }
     const LinDecay wl = lin_decay(c2, L);
 #pragma unroll
-    for (int m = 0; m < DA / 32; ++m) {
-      float4* d = reinterpret_cast<float4*>(&sm.s[tr + 32 * m][cg]);
+    for (int m = 0; m < RPT; ++m) {
+      float4* d = reinterpret_cast<float4*>(&sm.s[RPT * tr + m][cg]);
       const float4 v = *d;
       *d = make_float4(wl(v.x, up[m][0]), wl(v.y, up[m][1]), wl(v.z, up[m][2]), wl(v.w, up[m][3]));
     }
