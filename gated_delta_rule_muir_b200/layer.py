@@ -9,6 +9,8 @@ operands' device); what a call allocates is allocated for that stream.
 from __future__ import annotations
 
 import ctypes as C
+import functools
+import inspect
 
 import torch
 
@@ -49,35 +51,29 @@ def _io_code(t, name):
     return code
 
 
-class _On:
-    """The operands' device and the launch stream made current, for allocations and launches;
-    gives the stream's handle. The common call (the current device and its current stream)
-    switches nothing."""
+def _placed(fn):
+    """Runs fn with `stream` (default: the current stream of the first operand's device) as a raw
+    handle, that device and stream being current for its allocations and launches. The common
+    call, the current device and its current stream, switches nothing."""
+    first = next(iter(inspect.signature(fn).parameters))
 
-    __slots__ = ("device", "stream", "guards")
-
-    def __init__(self, device, stream):
-        self.device, self.stream, self.guards = device, stream, ()
-
-    def __enter__(self):
-        device, stream = self.device, self.stream
-        if device.type != "cuda":
-            raise ValueError(f"operands must be CUDA tensors, got {device}")
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        t = args[0] if args else kw.get(first)
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{first}: expected a tensor, got {type(t).__name__}")
+        if not t.is_cuda:
+            return fn(*args, stream=0, **kw)  # which refuses it
+        index = t.get_device()
         if stream is None:
-            if device.index == torch.cuda.current_device():
-                return _raw_stream(device.index)
-            stream = torch.cuda.current_stream(device)
-        elif stream.device != device:
-            raise ValueError(f"stream of {stream.device}, operands on {device}")
-        self.guards = (torch.cuda.device(device), torch.cuda.stream(stream))
-        for g in self.guards:
-            g.__enter__()
-        return stream.cuda_stream
-
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
-        return False
+            if index == torch.cuda.current_device():
+                return fn(*args, stream=_raw_stream(index), **kw)
+            stream = torch.cuda.current_stream(index)
+        elif stream.device_index != index:
+            raise ValueError(f"stream of {stream.device}, operands on {t.device}")
+        with torch.cuda.device(index), torch.cuda.stream(stream):
+            return fn(*args, stream=stream.cuda_stream, **kw)
+    return call
 
 
 def _workspace(nbytes, device, ws):
@@ -88,6 +84,14 @@ def _workspace(nbytes, device, ws):
     if ws.numel() * ws.element_size() < nbytes:
         raise ValueError("workspace too small")
     return ws
+
+
+def _like(t, name, x):
+    """The output `name`, shaped and typed like x."""
+    if t is None:
+        return torch.empty_like(x)
+    _need(t, name, x.shape, x.dtype, x.device)
+    return t
 
 
 def _out(t, name, shape, dtype, device):
@@ -122,6 +126,7 @@ def lin_attn_workspace_bytes(q, k, v, log_decay, *, backward=False) -> int:
     return int((lib.muir_lin_bwd_workspace if backward else lib.muir_lin_fwd_workspace)(C.byref(a)))
 
 
+@_placed
 def lin_attn_fwd(q, k, v, log_decay, *, scale=1.0, lengths=None, S0=None, want_state=True, y=None, S_T=None,
                  workspace=None, stream=None):
     """Linear attention with one decay per head, S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T,
@@ -132,15 +137,15 @@ def lin_attn_fwd(q, k, v, log_decay, *, scale=1.0, lengths=None, S0=None, want_s
     no gradient."""
     a, (B, T, H, dk, dv, dt, dev) = _lin_args(q, k, v, log_decay, scale, lengths, S0)
     lib = N.load()
-    with _On(dev, stream) as s:
-        y = _out(y, "y", (B, T, H, dv), dt, dev)
-        S_T = _out(S_T, "S_T", (B, H, dk, dv), torch.float32, dev) if want_state else None
-        nbytes = int(lib.muir_lin_fwd_workspace(C.byref(a)))
-        ws = _workspace(nbytes, dev, workspace)
-        N.check(lib.muir_lin_fwd(C.byref(a), _ptr(y), _ptr(S_T), _ptr(ws), nbytes, s), "muir_lin_fwd")
+    y = _like(y, "y", v)
+    S_T = _out(S_T, "S_T", (B, H, dk, dv), torch.float32, dev) if want_state else None
+    nbytes = int(lib.muir_lin_fwd_workspace(C.byref(a)))
+    ws = _workspace(nbytes, dev, workspace)
+    N.check(lib.muir_lin_fwd(C.byref(a), _ptr(y), _ptr(S_T), _ptr(ws), nbytes, stream), "muir_lin_fwd")
     return y, S_T
 
 
+@_placed
 def lin_attn_bwd(q, k, v, log_decay, dy, *, scale=1.0, lengths=None, S0=None, dS_T=None, want_dS0=True, outputs=None,
                  workspace=None, stream=None):
     """Gradients of lin_attn_fwd: a dict of dq, dk, dv (shaped and typed like q, k, v) and dS0
@@ -151,17 +156,17 @@ def lin_attn_bwd(q, k, v, log_decay, dy, *, scale=1.0, lengths=None, S0=None, dS
         _need(dS_T, "dS_T", (B, H, dk, dv), torch.float32, dev)
     lib = N.load()
     o = outputs or {}
-    with _On(dev, stream) as s:
-        out = {"dq": _out(o.get("dq"), "dq", (B, T, H, dk), dt, dev), "dk": _out(o.get("dk"), "dk", (B, T, H, dk), dt, dev),
-               "dv": _out(o.get("dv"), "dv", (B, T, H, dv), dt, dev),
-               "dS0": _out(o.get("dS0"), "dS0", (B, H, dk, dv), torch.float32, dev) if want_dS0 else None}
-        g = N.LinGrads(dy.data_ptr(), _ptr(dS_T), *(_ptr(out[n]) for n in ("dq", "dk", "dv", "dS0")))
-        nbytes = int(lib.muir_lin_bwd_workspace(C.byref(a)))
-        ws = _workspace(nbytes, dev, workspace)
-        N.check(lib.muir_lin_bwd(C.byref(a), C.byref(g), _ptr(ws), nbytes, s), "muir_lin_bwd")
+    out = {"dq": _like(o.get("dq"), "dq", q), "dk": _like(o.get("dk"), "dk", k),
+           "dv": _like(o.get("dv"), "dv", v),
+           "dS0": _out(o.get("dS0"), "dS0", (B, H, dk, dv), torch.float32, dev) if want_dS0 else None}
+    g = N.LinGrads(dy.data_ptr(), _ptr(dS_T), *(_ptr(out[n]) for n in ("dq", "dk", "dv", "dS0")))
+    nbytes = int(lib.muir_lin_bwd_workspace(C.byref(a)))
+    ws = _workspace(nbytes, dev, workspace)
+    N.check(lib.muir_lin_bwd(C.byref(a), C.byref(g), _ptr(ws), nbytes, stream), "muir_lin_bwd")
     return out
 
 
+@_placed
 def lin_attn_step(S, q, k, v, log_decay, *, scale=1.0, y=None, stream=None):
     """One token of lin_attn_fwd for n sequences: S [n,H,dk,dv] fp32 updated in place, q, k
     [n,H,dk], v [n,H,dv]. Returns y [n,H,dv]."""
@@ -173,11 +178,10 @@ def lin_attn_step(S, q, k, v, log_decay, *, scale=1.0, y=None, stream=None):
         _need(t, name, (n, H, d), q.dtype, dev)
     _need(log_decay, "log_decay", (H,), torch.float32, dev)
     lib = N.load()
-    with _On(dev, stream) as s:
-        y = _out(y, "y", (n, H, dv), q.dtype, dev)
-        a = N.LinStepArgs(n, H, dk, dv, code, float(scale), S.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                          log_decay.data_ptr(), y.data_ptr())
-        N.check(lib.muir_lin_step(C.byref(a), s), "muir_lin_step")
+    y = _like(y, "y", v)
+    a = N.LinStepArgs(n, H, dk, dv, code, float(scale), S.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                      log_decay.data_ptr(), y.data_ptr())
+    N.check(lib.muir_lin_step(C.byref(a), stream), "muir_lin_step")
     return y
 
 
@@ -192,37 +196,38 @@ def _norm_operands(x, weight, residual):
     return n, d, dev, code
 
 
+@_placed
 def rms_norm(x, weight, *, residual=None, eps=1e-6, y=None, h=None, rstd=None, stream=None):
     """RMS norm of rows x [n,d] (fp32 or bf16), weight [d] fp32, with the residual's addition:
     h = x + residual, y = h (mean h^2 + eps)^(-1/2) weight. Returns a dict of y, rstd [n] fp32
     and, with a residual, h (the new residual stream; may be the residual's own buffer)."""
     n, d, dev, code = _norm_operands(x, weight, residual)
     lib = N.load()
-    with _On(dev, stream) as s:
-        out = {"y": _out(y, "y", (n, d), x.dtype, dev), "rstd": _out(rstd, "rstd", (n,), torch.float32, dev)}
-        if residual is not None:
-            out["h"] = _out(h, "h", (n, d), x.dtype, dev)
-        N.check(lib.muir_rms_norm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(out["y"]), _ptr(out.get("h")), _ptr(out["rstd"]),
-                                  n, d, float(eps), code, s), "muir_rms_norm")
+    out = {"y": _like(y, "y", x), "rstd": _out(rstd, "rstd", (n,), torch.float32, dev)}
+    if residual is not None:
+        out["h"] = _like(h, "h", x)
+    N.check(lib.muir_rms_norm(_ptr(x), _ptr(residual), _ptr(weight), _ptr(out["y"]), _ptr(out.get("h")), _ptr(out["rstd"]),
+                              n, d, float(eps), code, stream), "muir_rms_norm")
     return out
 
 
+@_placed
 def rms_norm_quant(x, weight, *, residual=None, eps=1e-6, q=None, scale=None, h=None, rstd=None, stream=None):
     """rms_norm with its output in 8 bits: q [n,d] float8_e4m3fn and scale [n] fp32, q scale ~ y,
     scale = max |y| / 448 of the row. Returns a dict of q, scale, rstd and, with a residual, h."""
     n, d, dev, code = _norm_operands(x, weight, residual)
     lib = N.load()
-    with _On(dev, stream) as s:
-        out = {"q": _out(q, "q", (n, d), _E4M3, dev), "scale": _out(scale, "scale", (n,), torch.float32, dev),
-               "rstd": _out(rstd, "rstd", (n,), torch.float32, dev)}
-        if residual is not None:
-            out["h"] = _out(h, "h", (n, d), x.dtype, dev)
-        N.check(lib.muir_rms_norm_quant(_ptr(x), _ptr(residual), _ptr(weight), _ptr(out["q"]), _ptr(out["scale"]),
-                                        _ptr(out.get("h")), _ptr(out["rstd"]), n, d, float(eps), code, s),
-                "muir_rms_norm_quant")
+    out = {"q": _out(q, "q", (n, d), _E4M3, dev), "scale": _out(scale, "scale", (n,), torch.float32, dev),
+           "rstd": _out(rstd, "rstd", (n,), torch.float32, dev)}
+    if residual is not None:
+        out["h"] = _like(h, "h", x)
+    N.check(lib.muir_rms_norm_quant(_ptr(x), _ptr(residual), _ptr(weight), _ptr(out["q"]), _ptr(out["scale"]),
+                                    _ptr(out.get("h")), _ptr(out["rstd"]), n, d, float(eps), code, stream),
+            "muir_rms_norm_quant")
     return out
 
 
+@_placed
 def rms_norm_bwd(dy, h, weight, rstd, *, dh=None, dx=None, dweight=None, workspace=None, stream=None):
     """Gradients of rms_norm from its h (its x, without a residual) and rstd: (dx [n,d], dweight
     [d] fp32). dx is the gradient of x and of the residual alike; dh is the cotangent of h."""
@@ -236,16 +241,16 @@ def rms_norm_bwd(dy, h, weight, rstd, *, dh=None, dx=None, dweight=None, workspa
     if dh is not None:
         _need(dh, "dh", (n, d), h.dtype, dev)
     lib = N.load()
-    with _On(dev, stream) as s:
-        dx = _out(dx, "dx", (n, d), h.dtype, dev)
-        dweight = _out(dweight, "dweight", (d,), torch.float32, dev)
-        nbytes = int(lib.muir_rms_norm_bwd_workspace(n, d))
-        ws = _workspace(nbytes, dev, workspace)
-        N.check(lib.muir_rms_norm_bwd(_ptr(dy), _ptr(h), _ptr(weight), _ptr(rstd), _ptr(dh), _ptr(dx), _ptr(dweight), n, d,
-                                      code, _ptr(ws), nbytes, s), "muir_rms_norm_bwd")
+    dx = _like(dx, "dx", h)
+    dweight = _out(dweight, "dweight", (d,), torch.float32, dev)
+    nbytes = int(lib.muir_rms_norm_bwd_workspace(n, d))
+    ws = _workspace(nbytes, dev, workspace)
+    N.check(lib.muir_rms_norm_bwd(_ptr(dy), _ptr(h), _ptr(weight), _ptr(rstd), _ptr(dh), _ptr(dx), _ptr(dweight), n, d,
+                                  code, _ptr(ws), nbytes, stream), "muir_rms_norm_bwd")
     return dx, dweight
 
 
+@_placed
 def w4_quantize(w, *, group=128, stream=None):
     """Weights [O,K] (fp32 or bf16) to 4 bits: (codes [O,K] uint8 in 0..15, scales [O,K/group]
     bf16), w ~ scale (code - 8), scale = max |w| / 7 of each group."""
@@ -256,13 +261,13 @@ def w4_quantize(w, *, group=128, stream=None):
     if group not in (32, 64, 128) or K % 128:
         raise ValueError(f"group must be 32, 64 or 128 and K a multiple of 128 (got {group}, {K})")
     lib = N.load()
-    with _On(dev, stream) as s:
-        codes = torch.empty(O, K, dtype=torch.uint8, device=dev)
-        scales = torch.empty(O, K // group, dtype=torch.bfloat16, device=dev)
-        N.check(lib.muir_w4_quantize(_ptr(w), _ptr(codes), _ptr(scales), K, O, group, code, s), "muir_w4_quantize")
+    codes = torch.empty(O, K, dtype=torch.uint8, device=dev)
+    scales = torch.empty(O, K // group, dtype=torch.bfloat16, device=dev)
+    N.check(lib.muir_w4_quantize(_ptr(w), _ptr(codes), _ptr(scales), K, O, group, code, stream), "muir_w4_quantize")
     return codes, scales
 
 
+@_placed
 def w4_pack(codes, scales, *, stream=None):
     """Codes [O,K] uint8 and scales [O,K/group] bf16 in the layout of w4_matvec: (wq uint8
     [ceil(O/16), K/128, 1024], ws bf16 [ceil(O/16), K/128, 128/group, 16]); see include/muir.h."""
@@ -276,13 +281,13 @@ def w4_pack(codes, scales, *, stream=None):
     _need(scales, "scales", (O, ng), torch.bfloat16, dev)
     lib = N.load()
     tiles = (O + 15) // 16
-    with _On(dev, stream) as s:
-        wq = torch.empty(tiles, K // 128, 1024, dtype=torch.uint8, device=dev)
-        ws = torch.empty(tiles, K // 128, 128 // group, 16, dtype=torch.bfloat16, device=dev)
-        N.check(lib.muir_w4_pack(_ptr(codes), _ptr(scales), _ptr(wq), _ptr(ws), K, O, group, s), "muir_w4_pack")
+    wq = torch.empty(tiles, K // 128, 1024, dtype=torch.uint8, device=dev)
+    ws = torch.empty(tiles, K // 128, 128 // group, 16, dtype=torch.bfloat16, device=dev)
+    N.check(lib.muir_w4_pack(_ptr(codes), _ptr(scales), _ptr(wq), _ptr(ws), K, O, group, stream), "muir_w4_pack")
     return wq, ws
 
 
+@_placed
 def w4_matvec(x, wq, ws, O, *, x_scale=None, out_dtype=None, y=None, stream=None):
     """y [n,O] = x [n,K] times the transposed 4-bit weights (wq, ws of w4_pack, O outputs). x:
     fp32 or bf16 (y of the same type), or float8_e4m3fn with x_scale [n] fp32, as rms_norm_quant
@@ -308,8 +313,7 @@ def w4_matvec(x, wq, ws, O, *, x_scale=None, out_dtype=None, y=None, stream=None
             raise ValueError("x_scale belongs to 8-bit rows")
         _need(x_scale, "x_scale", (n,), torch.float32, dev)
     lib = N.load()
-    with _On(dev, stream) as s:
-        y = _out(y, "y", (n, O), ydt, dev)
-        N.check(lib.muir_w4_matvec(_ptr(x), _ptr(x_scale), _ptr(wq), _ptr(ws), _ptr(y), n, K, O, 128 // gpb, code,
-                                   N.MUIR_F32 if ydt == torch.float32 else N.MUIR_BF16, s), "muir_w4_matvec")
+    y = _out(y, "y", (n, O), ydt, dev)
+    N.check(lib.muir_w4_matvec(_ptr(x), _ptr(x_scale), _ptr(wq), _ptr(ws), _ptr(y), n, K, O, 128 // gpb, code,
+                               N.MUIR_F32 if ydt == torch.float32 else N.MUIR_BF16, stream), "muir_w4_matvec")
     return y

@@ -152,3 +152,14 @@ def test_the_binding_refuses_host_tensors_and_wrong_shapes():
         muir.w4_pack(z(4, 100, dtype=torch.uint8), z(4, 1, dtype=torch.bfloat16))
     with pytest.raises(ValueError, match="tiles"):
         muir.w4_matvec(z(1, 128), z(1, 1, 1024, dtype=torch.uint8), z(1, 1, 1, 16, dtype=torch.bfloat16), 17)
+
+
+def test_the_binding_takes_its_operands_by_name_and_only_tensors():
+    z = torch.zeros
+    with pytest.raises(ValueError, match="x: must be a contiguous CUDA tensor"):
+        muir.rms_norm(weight=z(8), x=z(2, 8))
+    for bad in (None, [1.0], 3):
+        with pytest.raises(TypeError, match="expected a tensor"):
+            muir.rms_norm(bad, z(8))
+    with pytest.raises(TypeError, match="expected a tensor"):
+        muir.w4_matvec()
