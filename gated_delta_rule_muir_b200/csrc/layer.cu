@@ -59,33 +59,37 @@ bool lin_use_tc(const muir_lin_args* a) {
   return a->dtype == MUIR_BF16 && a->T > 0 && (int64_t)a->H * a->dk >= 64 && (int64_t)a->H * a->dv >= 64;
 }
 
-// Segments of the sequence: `passes` passes of output per (sequence, head) share a launch.
+// Segments of the sequence, for `outs` passes of outputs (in one launch) and `states`
+// passes of segment states (in another, where there is more than one segment).
 //
-// Tensor cores, one CTA per SM: the split with the least cost, in chunk times, of
-// the waves of CTAs (each with a start and an end worth about 3 chunks), the
-// segments' own states where there is more than one (which read two of three
-// operands again: half as much again) and the walk over them.
+// Tensor cores, one CTA per SM: the split with the least cost, in times of a chunk of
+// outputs: the waves of CTAs times their chunks and a start worth 2 chunks, a chunk
+// of the segments' own states counting 0.55 (2.0 against 3.9 us at d = 128), and the
+// walk over the segments. One sequence of 32768 tokens and 16 heads: 9 segments, one
+// wave each, in the forward pass; the backward's 432 and 288 CTAs of 9 segments (3
+// and 2 waves) take 130 units, 144 and 96 CTAs of 3 segments 137.
 //
 // CUDA cores: two CTAs for each SM, at least 2 runs per segment.
-LinPlan lin_plan(const muir_lin_args* a, int passes) {
+LinPlan lin_plan(const muir_lin_args* a, int outs, int states) {
   LinPlan pl{lin_use_tc(a), 1, 0};
   const int64_t run = pl.tc ? muir::kLtChunk : muir::kLinRun;
   const int64_t runs = a->T > 0 ? (a->T + run - 1) / run : 1;
   int64_t n = 1;
   if (pl.tc) {
-    const int64_t units = a->B * a->H * passes;
+    const int64_t units = a->B * a->H;
     double best = 0.0;
     for (int64_t c = 1; c <= runs && c <= 1024; ++c) {
-      const double waves = (double)((units * c + kSMs - 1) / kSMs);
-      const double cost = waves * ((double)((runs + c - 1) / c) * (c > 1 ? 1.5 : 1.0) + 3.0) + (c > 1 ? 4.0 + 0.1 * (double)c : 0.0);
+      const double chunks = (double)((runs + c - 1) / c);
+      const auto waves = [&](int passes) { return (double)((units * passes * c + kSMs - 1) / kSMs); };
+      const double cost = waves(outs) * (chunks + 2.0) + (c > 1 ? waves(states) * (0.55 * chunks + 2.0) + 2.0 + 0.1 * (double)c : 0.0);
       if (c == 1 || cost < best) {
         best = cost;
         n = c;
       }
     }
   } else {
-    const int dmin = a->dk < a->dv && passes > 1 ? a->dk : a->dv;
-    const int64_t units = a->B * a->H * (dmin / 32) * passes;
+    const int dmin = a->dk < a->dv && outs > 1 ? a->dk : a->dv;
+    const int64_t units = a->B * a->H * (dmin / 32) * outs;
     n = (2 * kSMs + units - 1) / units;
     if (n > runs / 2) n = runs / 2;
     if (n < 1) n = 1;
@@ -195,7 +199,7 @@ int lin_run(const LinPlan& pl, int dtype, const muir::LinPass* states, int ns, c
     for (int i = 0; i < ns; ++i) ca.p[i] = states[i];
     const muir::LinPass& p = states[0];
     LaunchScope l("lin_combine", s);
-    muir::lin_combine_kernel<<<dim3((unsigned)(p.da * p.dc / 128), (unsigned)(p.B * p.H), (unsigned)ns), 128, 0, s>>>(ca);
+    muir::lin_combine_kernel<<<dim3((unsigned)((p.da * p.dc + 511) / 512), (unsigned)(p.B * p.H), (unsigned)ns), 128, 0, s>>>(ca);
     if ((rc = check_launch("lin_combine"))) return rc;
   }
   if (pl.tc) {
@@ -228,7 +232,7 @@ extern "C" {
 size_t muir_lin_fwd_workspace(const muir_lin_args* a) {
   muir_host::clear_error();
   if (lin_validate(a, "lin_fwd") || lin_empty(a)) return 0;
-  return lin_seg_bytes(a, lin_plan(a, 1));
+  return lin_seg_bytes(a, lin_plan(a, 1, 1));
 }
 
 int muir_lin_fwd(const muir_lin_args* a, void* y, float* S_T, void* ws, size_t ws_bytes, void* stream) {
@@ -239,7 +243,7 @@ int muir_lin_fwd(const muir_lin_args* a, void* y, float* S_T, void* ws, size_t w
   if ((rc = lin_pointers(a, "lin_fwd"))) return rc;
   const Ptr outs[] = {{y, "y", a->T == 0}, {S_T, "S_T", true}};
   if ((rc = check_ptrs("lin_fwd", outs))) return rc;
-  const LinPlan pl = lin_plan(a, 1);
+  const LinPlan pl = lin_plan(a, 1, 1);
   const size_t need = lin_seg_bytes(a, pl);
   if (need && (!ws || !aligned(ws, 256) || ws_bytes < need))
     return fail(MUIR_ERR_WORKSPACE, "lin_fwd: workspace needs %zu bytes, 256-byte aligned", need);
@@ -260,7 +264,7 @@ int muir_lin_fwd(const muir_lin_args* a, void* y, float* S_T, void* ws, size_t w
 size_t muir_lin_bwd_workspace(const muir_lin_args* a) {
   muir_host::clear_error();
   if (lin_validate(a, "lin_bwd") || lin_empty(a)) return 0;
-  const LinPlan pl = lin_plan(a, 3);
+  const LinPlan pl = lin_plan(a, 3, 2);
   return 2 * lin_seg_bytes(a, pl);
 }
 
@@ -278,7 +282,7 @@ int muir_lin_bwd(const muir_lin_args* a, const muir_lin_grads* g, void* ws, size
   // the passes run side by side: one may still read these while dS0 is written
   if (g->dS0 && (g->dS0 == g->dS_T || g->dS0 == a->S0))
     return fail(MUIR_ERR_INVALID_ARG, "lin_bwd: dS0 must not be dS_T's or S0's buffer");
-  const LinPlan pl = lin_plan(a, 3);
+  const LinPlan pl = lin_plan(a, 3, 2);
   const size_t seg = lin_seg_bytes(a, pl);
   if (seg && (!ws || !aligned(ws, 256) || ws_bytes < 2 * seg))
     return fail(MUIR_ERR_WORKSPACE, "lin_bwd: workspace needs %zu bytes, 256-byte aligned", 2 * seg);

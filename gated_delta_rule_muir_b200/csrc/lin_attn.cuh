@@ -82,39 +82,41 @@ __device__ __forceinline__ int64_t lin_seg_tokens(const LinPass& p, int64_t len,
 
 // ---- segment states -> states entering each segment ---------------------------
 //
-// One thread per state element and (b, h): a walk over the segments, in the
-// pass's direction, that replaces each segment's own state by the state that
-// enters it. Every load of the walk is independent, so four are kept in flight.
+// One thread per four state elements and (b, h): a walk over the segments, in the
+// pass's direction, that replaces each segment's own state by the state that enters
+// it. The loads of the walk are independent: eight are kept in flight.
 struct LinCombineArgs {
   LinPass p[2];
 };
 __global__ void __launch_bounds__(128) lin_combine_kernel(const __grid_constant__ LinCombineArgs args) {
   const LinPass& p = args.p[blockIdx.z];
   const int n = p.da * p.dc;
-  const int bh = blockIdx.y, e = blockIdx.x * 128 + threadIdx.x;
+  const int bh = blockIdx.y, e = (blockIdx.x * 128 + threadIdx.x) * 4;
   if (e >= n) return;
   const int b = bh / p.H, h = bh % p.H;
   const float c = lin_log2(p.log_decay, h);
   const int64_t len = lin_length(p, b);
-  float s = p.init ? __ldg(p.init + (int64_t)bh * n + e) : 0.f;
+  float4 s = p.init ? __ldg(reinterpret_cast<const float4*>(p.init + (int64_t)bh * n + e)) : make_float4(0.f, 0.f, 0.f, 0.f);
   float* q = p.seg + (int64_t)bh * p.nseg * n + e;
   const int64_t step = p.reverse ? -n : n;
   if (p.reverse) q += (int64_t)(p.nseg - 1) * n;
-  constexpr int U = 4;
+  constexpr int U = 8;
   for (int j0 = 0; j0 < p.nseg; j0 += U) {
-    float own[U];
+    float4 own[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) own[u] = j0 + u < p.nseg ? q[u * step] : 0.f;
+    for (int u = 0; u < U; ++u)
+      if (j0 + u < p.nseg) own[u] = *reinterpret_cast<const float4*>(q + u * step);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (j0 + u >= p.nseg) break;
-      q[u * step] = s;
+      *reinterpret_cast<float4*>(q + u * step) = s;
       const int j = p.reverse ? p.nseg - 1 - (j0 + u) : j0 + u;
-      s = lin_decay(c, lin_seg_tokens(p, len, j))(s, own[u]);
+      const LinDecay w = lin_decay(c, lin_seg_tokens(p, len, j));
+      s = make_float4(w(s.x, own[u].x), w(s.y, own[u].y), w(s.z, own[u].z), w(s.w, own[u].w));
     }
     q += U * step;
   }
-  if (p.fin) p.fin[(int64_t)bh * n + e] = s;
+  if (p.fin) *reinterpret_cast<float4*>(p.fin + (int64_t)bh * n + e) = s;
 }
 
 // ---- CUDA-core pass -----------------------------------------------------------

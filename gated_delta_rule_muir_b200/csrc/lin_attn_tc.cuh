@@ -589,14 +589,19 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       }
 #pragma unroll
       for (int j = 0; j < 64; ++j) S[j] = 0.f;
-      if (src && mine) {
-        const int step = tr ? p.da : 1;  // between columns
-        src += tr ? (int64_t)(64 * half) * p.da + r : (int64_t)r * p.dc + 64 * half;
+      if (src && mine && tr) {
+        src += (int64_t)(64 * half) * p.da + r;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) S[j] = __ldg(src + j * step);
-        if (scols == 64) {
+        for (int j = 0; j < 64; ++j)
+          if (j < scols) S[j] = __ldg(src + j * p.da);
+      } else if (src && mine) {
+        src += (int64_t)r * p.dc + 64 * half;
 #pragma unroll
-          for (int j = 32; j < 64; ++j) S[j] = __ldg(src + j * step);
+        for (int j = 0; j < 64; j += 4) {
+          if (j < scols) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(src + j));
+            S[j] = v.x; S[j + 1] = v.y; S[j + 2] = v.z; S[j + 3] = v.w;
+          }
         }
       }
     }
