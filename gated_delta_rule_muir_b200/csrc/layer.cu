@@ -516,13 +516,16 @@ void w4_launch(const muir::W4Params& p, int group, cudaStream_t s) {
   else if (group == 64) muir::w4_matvec_kernel<X, Y, NB, 2, RT><<<grid, 32 * muir::kW4Warps, 0, s>>>(p);
   else muir::w4_matvec_kernel<X, Y, NB, 1, RT><<<grid, 32 * muir::kW4Warps, 0, s>>>(p);
 }
-// Four tiles of outputs per CTA once that still makes four CTAs for each SM: then x
-// is converted a quarter as often (50257 x 2048, eight e4m3 rows: 24 -> W4_WIDE us);
-// with fewer outputs one tile each, for more CTAs (6144 x 2048, one row: see there).
+// Two tiles of outputs per CTA where that still makes eight CTAs for each SM: x is
+// then fetched and converted half as often. K = 2048, two tiles against one: 50257
+// outputs of eight e4m3 rows 17.4 against 18.8 us, 30000 12.9 both, 16384 7.2 against
+// 6.9, 6144 of one bf16 row 4.5 against 3.8. More than 16 rows take one tile (registers).
 template <typename X, typename Y, int NB>
 void w4_go(const muir::W4Params& p, int group, cudaStream_t s) {
-  if (NB <= 2 && (p.O + 15) / 16 >= 16 * kSMs) w4_launch<X, Y, NB, NB <= 2 ? 2 : 1>(p, group, s);
-  else w4_launch<X, Y, NB, 1>(p, group, s);
+  if constexpr (NB <= 2) {
+    if ((p.O + 15) / 16 >= 16 * kSMs) return w4_launch<X, Y, NB, 2>(p, group, s);
+  }
+  w4_launch<X, Y, NB, 1>(p, group, s);
 }
 template <typename X, typename Y>
 void w4_rows(const muir::W4Params& p, int group, cudaStream_t s) {

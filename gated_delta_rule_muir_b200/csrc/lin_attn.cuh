@@ -126,7 +126,8 @@ __global__ void __launch_bounds__(128) lin_combine_kernel(const __grid_constant_
 // in fp32. The products are recomputed by each of the dc / 32 slabs, a third of the
 // arithmetic at da = dc = 128. Bound by shared-memory reads: the tiles (4 x 4 scores,
 // 2 x 4 outputs and da / 32 x 4 state elements per thread, all read four floats at a
-// time) take about seven products for each 16-byte read.
+// time) take about seven products for each 16-byte read. Backward of 2 x 777 tokens, 4
+// heads of 64: 70 us a call, three launches.
 constexpr int kLinRun = 64;
 
 constexpr int kLinMaxPasses = 3;
@@ -319,7 +320,8 @@ __global__ void __launch_bounds__(256) lin_simt_kernel(const __grid_constant__ L
 //
 // y_j = scale (lambda sum_i q_i S_ij + (q . k) v_j), S_ij <- lambda S_ij + k_i v_j.
 // Memory bound: one CTA per (sequence, head, 32 columns) reads its slab of the
-// state once into registers and writes it once, as the gated-delta-rule step does.
+// state once into registers and writes it once, as the gated-delta-rule step does
+// (1536 sequences x 16 heads of 128 x 128: 475 us, 6.8 TB/s).
 struct LinStepParams {
   float* S;
   const void *q, *k, *v;

@@ -25,10 +25,17 @@
 // two parts, 17 bits, by three packed bf16 operations for two elements.
 //
 // Bound: per chunk 128 KB of operands and output, about 5700 cycles at this GPU's
-// copy bandwidth with one CTA per SM, against five products of 512 tensor cycles
-// (six with three parts) and about 3000 issue slots of each scheduler for the work
-// on elements. So the pass is bound by memory if the roles run side by side and the
-// next tiles are on their way, which is what the rest is for.
+// copy bandwidth with one CTA per SM; five products of 512 tensor cycles (six with
+// three parts); and shared memory, about 4600 cycles of its 128 bytes a cycle: the
+// products read 2300 cycles' worth (a 128 x 128 x 16 step with both operands in shared
+// memory takes all of it), copies in and out 1000, cutting 770, S and the outputs 500.
+// Measured, one sequence of 32768 tokens, 16 heads of 128: outputs 126 us (83 at the
+// copy bandwidth), the segments' own states 75 (42). With nearly all work on elements
+// left out of a timing copy the outputs took 105 us, and no single role's work moved
+// them by more than 10: what is left is the traffic and the hand-offs, not one stage.
+// Slower were: masking in unrolled blocks of 32 columns (237 us for both launches
+// against 220: such code runs at the pace of instruction fetches), outputs stored a
+// row per thread, tiles asked into L2 two chunks ahead, y2 issued before the parts.
 //
 // Shared memory, 7 tiles of 32 KB: a ring of four for b, a, c (b first: it is cut
 // ahead of everything else and its slot is free again as soon as it has been cut and
@@ -42,9 +49,10 @@
 // row, 64 columns per thread). The products are issued parts(n), y2(n), y1(n), scores(n+1):
 // the parts and y2 run while the scores are masked. The block is launched with 72
 // registers per thread; the warpgroups trade them (40 + 2 x 56 + 2 x 64 + 2 x 112 =
-// 7 x 72). Hand-offs are mbarriers with bounded waits:
-//   full[s], empty[s]   slot s holds a tile / its readers are done (one commit and
-//                       the eight cutting warps)
+// 7 x 72). Without outputs warps 4..19 cut (a quarter row per thread) and dS has two
+// buffers in TMEM. Hand-offs are mbarriers with bounded waits:
+//   full[s], empty[s]   slot s holds a tile / its readers are done (one commit and the
+//                       cutting warps, or for c the warps that write outputs over it)
 //   scores    scores in TMEM               (MMA -> mask, cut)
 //   weights   masked scores in TMEM        (mask -> MMA)
 //   y2, y     y2 / y1 and y2 in TMEM       (MMA -> state)
@@ -319,122 +327,107 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
   if (warp < 4) {
     regs_dec<40>();
     if (warp == 0) {
-    // ---- TMA: tiles in the order they are needed, b(n) a(n) c(n) b(n+1) .. --------
-    if (lane == 0) {
-      bool ok = true;
-      int m = 0;
-      auto map_of = [&](int k) { return k == 0 ? &args.b[pi] : k == TILES - 1 ? &args.c[pi] : &args.a[pi]; };
-      auto width = [&](int k) { return k == TILES - 1 ? p.dc : p.da; };
-      auto first = [&](int n) { return (int)(u.t0 + (int64_t)chunk_at(n) * kLtChunk); };
-      for (int n = 0; n < u.chunks && ok; ++n) {
-        for (int k = 0; k < TILES && ok; ++k, ++m) {
-          const int s = m % SLOTS, turn = m / SLOTS;
-          if (turn > 0) ok = lane_wait(&empty[s], (uint32_t)(turn - 1) & 1u);
-          if (!ok) break;
-          const int d = width(k);
-          const uint32_t dst = base + (uint32_t)s * kLtTile;
-          mbar_expect_tx(&full[s], d > 64 ? 2u * kLtBox : kLtBox);
-          for (int x = 0; x < d; x += 64)
-            tma_load_3d(dst + (x ? kLtBox : 0u), map_of(k), u.h * d + x, first(n), u.b, &full[s]);
+      // ---- TMA: tiles in the order they are needed, b(n) a(n) c(n) b(n+1) .. --------
+      if (lane == 0) {
+        bool ok = true;
+        int m = 0;
+        auto map_of = [&](int k) { return k == 0 ? &args.b[pi] : k == TILES - 1 ? &args.c[pi] : &args.a[pi]; };
+        auto width = [&](int k) { return k == TILES - 1 ? p.dc : p.da; };
+        auto first = [&](int n) { return (int)(u.t0 + (int64_t)chunk_at(n) * kLtChunk); };
+        for (int n = 0; n < u.chunks && ok; ++n) {
+          for (int k = 0; k < TILES && ok; ++k, ++m) {
+            const int s = m % SLOTS, turn = m / SLOTS;
+            if (turn > 0) ok = lane_wait(&empty[s], (uint32_t)(turn - 1) & 1u);
+            if (!ok) break;
+            const int d = width(k);
+            const uint32_t dst = base + (uint32_t)s * kLtTile;
+            mbar_expect_tx(&full[s], d > 64 ? 2u * kLtBox : kLtBox);
+            for (int x = 0; x < d; x += 64)
+              tma_load_3d(dst + (x ? kLtBox : 0u), map_of(k), u.h * d + x, first(n), u.b, &full[s]);
+          }
         }
+        // no copy is in flight when the CTA ends, even after a wait that ran out
+        for (int s = 0; s < SLOTS; ++s)
+          if (m > s) mbar_wait(&full[s], (uint32_t)((m - 1 - s) / SLOTS) & 1u);
       }
-      // no copy is in flight when the CTA ends, even after a wait that ran out
-      for (int s = 0; s < SLOTS; ++s)
-        if (m > s) mbar_wait(&full[s], (uint32_t)((m - 1 - s) / SLOTS) & 1u);
-    }
     } else if (warp == 1) {
-    // ---- MMA ------------------------------------------------------------------------
-    // The warp stays converged and one elected lane issues: slots, step counts and
-    // waits' results are the same in every lane and known to be (a vote, a warp
-    // reduction), so that the descriptors are formed in uniform registers. Issued
-    // from inside a one-lane branch, each product took three to four times as long.
-    const int chunks = (int)__reduce_max_sync(0xffffffffu, (unsigned)u.chunks);
-    const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
-    const uint32_t m_scores = tm, m_y1 = tm + 128, m_y2 = tm + 256;
-    if (elect_one()) {
-    bool ok = true;
-    const uint32_t id_scores = idesc_bf16(128, 128, 0, 0), id_y = idesc_bf16(128, p.dc, 0, 1),
-                   id_ds = idesc_bf16(128, p.dc, 1, 1);
-    auto slot = [&](int m) { return base + (uint32_t)(m % SLOTS) * kLtTile; };
-    auto landed = [&](int m) { return lane_wait(&full[m % SLOTS], (uint32_t)(m / SLOTS) & 1u); };
-    auto scores = [&](int n) {  // a b^T of chunk n; its TMEM columns hold chunk n - 1's weights until y1 is done
-      const int m = n * TILES;
-      if (!landed(m) || !landed(m + 1) || (n > 0 && !lane_wait(&b_y, (uint32_t)(n - 1) & 1u))) return false;
-      tc_fence_after();
-      {
-        lt_product_k<false>(p.da, m_scores, slot(m + 1), slot(m), id_scores);
-        mma_commit(&b_scores);
-        if (PARTS == 2) mma_commit(&empty[m % SLOTS]);
-      }
-      return true;
-    };
-    if (OUT && chunks > 0) ok = scores(0);
-    for (int n = 0; n < chunks && ok; ++n) {
-      const uint32_t ph = (uint32_t)n & 1u;
-      const int mb = n * TILES, ma = mb + 1, mc = mb + TILES - 1;
-      const uint32_t bt = slot(mb), ct = slot(mc), m_ds = tm + 384u - 128u * (uint32_t)ds_buf(n);
-      // c's tile: landed, and its rows past the last token cleared by the cutters
-      ok = landed(mc) && lane_wait(&b_cut, ph) && 
-           (n <= ds_buf(1) || lane_wait(&b_dsfree[ds_buf(n)], ds_phase(n) ^ 1u));
-      if (!ok) break;
-      tc_fence_after();
-      {
-        if (PARTS == 3) {
-          lt_product<8, false, true, true>(m_ds, part3(n, bt), ct, id_ds);
-          if (!OUT) mma_commit(&b_used3);
-          lt_product<8, true, true, true>(m_ds, part2(n, bt), ct, id_ds);
-        } else {
-          lt_product<8, false, true, true>(m_ds, part2(n, bt), ct, id_ds);
-        }
-        lt_product<8, true, true, true>(m_ds, part1(n, bt), ct, id_ds);
-        mma_commit(&b_ds[ds_buf(n)]);
-        if (PARTS == 3) mma_commit(&empty[mb % SLOTS]);
-        if (!OUT) mma_commit(&empty[mc % SLOTS]);
-      }
-      if (OUT) {
-        ok = lane_wait(&b_sready, ph) && (n == 0 || lane_wait(&b_yfree, ph ^ 1u));
-        if (!ok) break;
-        tc_fence_after();
-        {
-          lt_product_k<true>(p.da, m_y2, slot(ma), s_tile, id_y);
-          mma_commit(&b_y2);
-          mma_commit(&empty[ma % SLOTS]);
-        }
-        }
-      if (OUT) {
-        ok = lane_wait(&b_weights, ph);
-        if (!ok) break;
-        tc_fence_after();
-        {
-          const uint32_t cd = lt_desc(ct, kLtBox);
-          mma_step_ta<false>(m_y1, m_scores, cd, id_y);
+      // ---- MMA: one elected lane -----------------------------------------------------
+      const int chunks = (int)__reduce_max_sync(0xffffffffu, (unsigned)u.chunks);  // known to be the same in all lanes
+      const uint32_t tm = __reduce_max_sync(0xffffffffu, tmem);
+      if (elect_one()) {
+        const uint32_t m_scores = tm, m_y1 = tm + 128, m_y2 = tm + 256;
+        const uint32_t id_scores = idesc_bf16(128, 128, 0, 0), id_y = idesc_bf16(128, p.dc, 0, 1),
+                       id_ds = idesc_bf16(128, p.dc, 1, 1);
+        bool ok = true;
+        auto slot = [&](int m) { return base + (uint32_t)(m % SLOTS) * kLtTile; };
+        auto landed = [&](int m) { return lane_wait(&full[m % SLOTS], (uint32_t)(m / SLOTS) & 1u); };
+        auto scores = [&](int n) {  // a b^T of chunk n; its TMEM columns hold chunk n - 1's weights until y1 is done
+          const int m = n * TILES;
+          if (!landed(m) || !landed(m + 1) || (n > 0 && !lane_wait(&b_y, (uint32_t)(n - 1) & 1u))) return false;
+          tc_fence_after();
+          lt_product_k<false>(p.da, m_scores, slot(m + 1), slot(m), id_scores);
+          mma_commit(&b_scores);
+          if (PARTS == 2) mma_commit(&empty[m % SLOTS]);
+          return true;
+        };
+        if (OUT && chunks > 0) ok = scores(0);
+        for (int n = 0; n < chunks && ok; ++n) {
+          const uint32_t ph = (uint32_t)n & 1u;
+          const int mb = n * TILES, ma = mb + 1, mc = mb + TILES - 1;
+          const uint32_t bt = slot(mb), ct = slot(mc), m_ds = tm + 384u - 128u * (uint32_t)ds_buf(n);
+          // c's tile has landed, and the cutters have cleared its rows past the last token
+          ok = landed(mc) && lane_wait(&b_cut, ph) &&
+               (n <= ds_buf(1) || lane_wait(&b_dsfree[ds_buf(n)], ds_phase(n) ^ 1u));
+          if (!ok) break;
+          tc_fence_after();
+          if constexpr (PARTS == 3) {
+            lt_product<8, false, true, true>(m_ds, part3(n, bt), ct, id_ds);
+            if (!OUT) mma_commit(&b_used3);
+            lt_product<8, true, true, true>(m_ds, part2(n, bt), ct, id_ds);
+          } else {
+            lt_product<8, false, true, true>(m_ds, part2(n, bt), ct, id_ds);
+          }
+          lt_product<8, true, true, true>(m_ds, part1(n, bt), ct, id_ds);
+          mma_commit(&b_ds[ds_buf(n)]);
+          if (PARTS == 3) mma_commit(&empty[mb % SLOTS]);
+          if constexpr (!OUT) {
+            mma_commit(&empty[mc % SLOTS]);
+          } else {
+            ok = lane_wait(&b_sready, ph) && (n == 0 || lane_wait(&b_yfree, ph ^ 1u));
+            if (!ok) break;
+            tc_fence_after();
+            lt_product_k<true>(p.da, m_y2, slot(ma), s_tile, id_y);
+            mma_commit(&b_y2);
+            mma_commit(&empty[ma % SLOTS]);
+            ok = lane_wait(&b_weights, ph);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t cd = lt_desc(ct, kLtBox);
+            mma_step_ta<false>(m_y1, m_scores, cd, id_y);
 #pragma unroll
-          for (int j = 1; j < 8; ++j)
-            mma_step_ta<true>(m_y1, m_scores + (uint32_t)(16 * j), cd + lt_mnstep(j), id_y);
-          mma_commit(&b_y);
-          mma_commit(&empty[mc % SLOTS]);
+            for (int j = 1; j < 8; ++j) mma_step_ta<true>(m_y1, m_scores + (uint32_t)(16 * j), cd + lt_mnstep(j), id_y);
+            mma_commit(&b_y);
+            mma_commit(&empty[mc % SLOTS]);
+            if (n + 1 < chunks) ok = scores(n + 1);
+          }
         }
-          if (n + 1 < chunks) ok = scores(n + 1);
+        // every issued product has completed when the CTA ends: the last chunk's commits
+        // are waited for here, or after a wait that ran out one more commit is
+        if (ok) {
+          if (chunks > 0) {
+            lane_wait(&b_ds[ds_buf(chunks - 1)], ds_phase(chunks - 1));
+            if (OUT) lane_wait(&b_y, (uint32_t)(chunks - 1) & 1u);
+          }
+        } else {
+          mma_commit(&b_scores);
+          mbar_wait_for(&b_scores, 0u, 1000000ull);
+          mbar_wait_for(&b_scores, 1u, 1000000ull);
+        }
       }
-    }
-    // every issued product has completed when the CTA ends: the last chunk's commits
-    // are waited for here, or after a wait that ran out one more commit is
-    if (ok) {
-      if (chunks > 0) {
-        lane_wait(&b_ds[ds_buf(chunks - 1)], ds_phase(chunks - 1));
-        if (OUT) lane_wait(&b_y, (uint32_t)(chunks - 1) & 1u);
-      }
-    } else {
-      mma_commit(&b_scores);
-      mbar_wait_for(&b_scores, 0u, 1000000ull);
-      mbar_wait_for(&b_scores, 1u, 1000000ull);
-    }
-    }
     }
   } else if (OUT && warp < 12) {
     // ---- mask: thread = token row i of the chunk, every other 16 columns -------------------------
     regs_dec<56>();
-    if constexpr (OUT) {
     const int w = warp & 3, i = w * 32 + lane, c0 = warp < 8 ? 0 : 16;
     const uint32_t row = tmem_lane_base(warp);
     // 16 columns at a time in one short loop (an unrolled body of this size runs at the
@@ -493,7 +486,6 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive1(&b_weights);
-    }
     }
   } else if (warp < 20) {
     // ---- cut b: thread = half a token row --------------------------------------------------------
