@@ -69,7 +69,8 @@ bool lin_use_tc(const muir_lin_args* a) {
 // wave each, in the forward pass; the backward's 432 and 288 CTAs of 9 segments (3
 // and 2 waves) take 130 units, 144 and 96 CTAs of 3 segments 137.
 //
-// CUDA cores: two CTAs for each SM, at least 2 runs per segment.
+// CUDA cores: as many CTAs as fit beside one another, three for each SM up to 64
+// channels and two for 128.
 LinPlan lin_plan(const muir_lin_args* a, int outs, int states) {
   LinPlan pl{lin_use_tc(a), 1, 0};
   const int64_t run = pl.tc ? muir::kLtChunk : muir::kLinRun;
@@ -90,8 +91,9 @@ LinPlan lin_plan(const muir_lin_args* a, int outs, int states) {
   } else {
     const int dmin = a->dk < a->dv && outs > 1 ? a->dk : a->dv;
     const int64_t units = a->B * a->H * (dmin / 32) * outs;
-    n = (2 * kSMs + units - 1) / units;
-    if (n > runs / 2) n = runs / 2;
+    const int64_t fit = (a->dk > 64 || (outs > 1 && a->dv > 64) ? 2 : 3) * kSMs;
+    n = (fit + units - 1) / units;
+    if (n > runs) n = runs;
     if (n < 1) n = 1;
   }
   const int64_t per = (runs + n - 1) / n;

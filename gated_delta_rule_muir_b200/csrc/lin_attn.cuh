@@ -241,6 +241,7 @@ __global__ void __launch_bounds__(256) lin_simt_kernel(const __grid_constant__ L
           for (int m = 0; m < 4; ++m)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
+              if (p.reverse ? k >= m : k <= m)  // the others are masked
               acc[m][k] = fmaf(av[m].x, bv[k].x,
                                fmaf(av[m].y, bv[k].y, fmaf(av[m].z, bv[k].z, fmaf(av[m].w, bv[k].w, acc[m][k]))));
         }
@@ -255,12 +256,23 @@ __global__ void __launch_bounds__(256) lin_simt_kernel(const __grid_constant__ L
       }
       __syncthreads();
       float o[2][4] = {}, u[2][4] = {};
-#pragma unroll 4
-      for (int s = 0; s < kLinRun; s += 4) {
-        const float4 p0 = lds4(&sm.p[tr][s]), p1 = lds4(&sm.p[tr + 32][s]);
-        const float4 c0 = lds4(&sm.c[s][cg]), c1 = lds4(&sm.c[s + 1][cg]), c2v = lds4(&sm.c[s + 2][cg]), c3 = lds4(&sm.c[s + 3][cg]);
-        fma4(o[0], p0.x, c0); fma4(o[0], p0.y, c1); fma4(o[0], p0.z, c2v); fma4(o[0], p0.w, c3);
-        fma4(o[1], p1.x, c0); fma4(o[1], p1.y, c1); fma4(o[1], p1.z, c2v); fma4(o[1], p1.w, c3);
+      // rows tr take the first half of the tokens before them (in reverse: both halves),
+      // rows tr + 32 both (in reverse: the second)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const bool lower = p.reverse || half == 0, upper = !p.reverse || half == 1;
+#pragma unroll 2
+        for (int s = 32 * half; s < 32 * half + 32; s += 4) {
+          const float4 c0 = lds4(&sm.c[s][cg]), c1 = lds4(&sm.c[s + 1][cg]), c2v = lds4(&sm.c[s + 2][cg]), c3 = lds4(&sm.c[s + 3][cg]);
+          if (lower) {
+            const float4 p0 = lds4(&sm.p[tr][s]);
+            fma4(o[0], p0.x, c0); fma4(o[0], p0.y, c1); fma4(o[0], p0.z, c2v); fma4(o[0], p0.w, c3);
+          }
+          if (upper) {
+            const float4 p1 = lds4(&sm.p[tr + 32][s]);
+            fma4(o[1], p1.x, c0); fma4(o[1], p1.y, c1); fma4(o[1], p1.z, c2v); fma4(o[1], p1.w, c3);
+          }
+        }
       }
 #pragma unroll 4
       for (int e = 0; e < DA; e += 4) {

@@ -39,7 +39,8 @@
 //
 // Shared memory, 7 tiles of 32 KB: a ring of four for b, a, c (b first: it is cut
 // ahead of everything else and its slot is free again as soon as it has been cut and
-// multiplied), two for the parts, one for S. Third parts go over b itself. Without
+// multiplied), two for the parts, one for S. Third parts of 128 channels
+// go over b itself. Without
 // outputs: the ring for b, c, first parts over b, two tiles for second parts (even
 // and odd chunks) and one for third parts, which are multiplied first.
 //
@@ -293,7 +294,9 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
   const uint32_t spare = base + (uint32_t)SLOTS * kLtTile, s_tile = spare + 2u * kLtTile;
   auto part1 = [&](int n, uint32_t bt) { return OUT ? spare : bt; };
   auto part2 = [&](int n, uint32_t bt) { return spare + (OUT ? 1u : (uint32_t)(n & 1)) * kLtTile; };
-  auto part3 = [&](int n, uint32_t bt) { return OUT ? bt : spare + 2u * kLtTile; };
+  // third parts of 128 channels go over b, after the scores; of 64 they have room beside the first
+  const bool over_b = OUT && PARTS == 3 && p.da > 64;
+  auto part3 = [&](int n, uint32_t bt) { return !OUT ? spare + 2u * kLtTile : over_b ? bt : spare + kLtBox; };
   if (tid == 0) {
     for (int i = 0; i < SLOTS; ++i) {
       mbar_init(&full[i], 1);
@@ -367,7 +370,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
           tc_fence_after();
           lt_product_k<false>(p.da, m_scores, slot(m + 1), slot(m), id_scores);
           mma_commit(&b_scores);
-          if (PARTS == 2) mma_commit(&empty[m % SLOTS]);
+          if (!over_b) mma_commit(&empty[m % SLOTS]);
           return true;
         };
         if (OUT && chunks > 0) ok = scores(0);
@@ -389,7 +392,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
           }
           lt_product<8, true, true, true>(m_ds, part1(n, bt), ct, id_ds);
           mma_commit(&b_ds[ds_buf(n)]);
-          if (PARTS == 3) mma_commit(&empty[mb % SLOTS]);
+          if (!OUT || over_b) mma_commit(&empty[mb % SLOTS]);
           if constexpr (!OUT) {
             mma_commit(&empty[mc % SLOTS]);
           } else {
@@ -507,7 +510,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       if (L < kLtChunk) ok = ok && warp_wait(&full[mc % SLOTS], (uint32_t)(mc / SLOTS) & 1u);
       // the tiles of the last parts have been used; before third parts go over b, the scores have been formed
       if (n > 0) ok = ok && warp_wait(OUT ? &b_ds[0] : &b_used3, (uint32_t)(n - 1) & 1u);
-      if (OUT && PARTS == 3) ok = ok && warp_wait(&b_scores, (uint32_t)n & 1u);
+      if (over_b) ok = ok && warp_wait(&b_scores, (uint32_t)n & 1u);
       if (!ok) break;
       // packed bf16, two parts: with the weight as w1 + w2, p1 = b w1 rounded, and
       // p2 = (b w1 - p1) + b w2, the bracket exact, rounded once
