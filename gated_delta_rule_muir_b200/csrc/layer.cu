@@ -393,16 +393,17 @@ void norm_go(const muir::NormParams& p, cudaStream_t s) {
   if (NT > 32) muir::rms_norm_kernel<T, NT, V, QUANT><<<(unsigned)p.n, NT, 0, s>>>(p);
   else muir::rms_norm_kernel<T, NT, V, QUANT><<<(unsigned)((p.n + 7) / 8), 256, 0, s>>>(p);
 }
-// Threads per row: a warp up to 1024 elements, else the fewest warps that hold the
-// row at one piece of 8 per thread, two pieces above 8192.
+// Threads per row: a warp up to 1024 elements; above that two pieces of 8 per thread
+// (32768 x 2048 bf16 with the residual, before the loads were moved ahead of the
+// stores: 88 us with 128 threads, 94 with 256 and one piece, 101 with 64 and four).
 template <typename T, bool QUANT>
 void norm_dispatch(const muir::NormParams& p, cudaStream_t s) {
   if (p.d <= 256) norm_go<T, 32, 1, QUANT>(p, s);
   else if (p.d <= 512) norm_go<T, 32, 2, QUANT>(p, s);
   else if (p.d <= 1024) norm_go<T, 32, 4, QUANT>(p, s);
-  else if (p.d <= 2048) norm_go<T, 256, 1, QUANT>(p, s);
-  else if (p.d <= 4096) norm_go<T, 512, 1, QUANT>(p, s);
-  else if (p.d <= 8192) norm_go<T, 1024, 1, QUANT>(p, s);
+  else if (p.d <= 2048) norm_go<T, 128, 2, QUANT>(p, s);
+  else if (p.d <= 4096) norm_go<T, 256, 2, QUANT>(p, s);
+  else if (p.d <= 8192) norm_go<T, 512, 2, QUANT>(p, s);
   else norm_go<T, 1024, 2, QUANT>(p, s);
 }
 
