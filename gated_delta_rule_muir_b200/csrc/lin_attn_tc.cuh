@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       const __nv_bfloat16 w1 = __float2bfloat16_rn(wt), w2 = __float2bfloat16_rn(wt - __bfloat162float(w1));
       const __nv_bfloat162 w11 = __halves2bfloat162(w1, w1), w22 = __halves2bfloat162(w2, w2);
       if (8 * q0 < p.da) {
-#pragma unroll 2
+#pragma unroll 4
         for (int c = k0; c < k0 + PIECES; ++c) {
           const uint32_t at = (uint32_t)((c ^ (r & 7)) << 4);
           uint4 v = *reinterpret_cast<const uint4*>(__cvta_shared_to_generic(line + at));
