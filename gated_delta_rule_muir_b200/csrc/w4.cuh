@@ -42,18 +42,26 @@ struct W4Params {
   int K, O;
 };
 
-template <bool HALF>
+// d = a b + (FIRST ? 0 : d)
+template <bool HALF, bool FIRST>
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if constexpr (HALF)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+#define MUIR_MMA(TYPE)                                                                                                   \
+  if constexpr (FIRST)                                                                                                   \
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE                                                  \
+                 ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"                                        \
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])                                                        \
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));                              \
+  else                                                                                                                   \
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE                                                  \
+                 ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"                                            \
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])                                                        \
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1))
+  if constexpr (HALF) {
+    MUIR_MMA("f16");
+  } else {
+    MUIR_MMA("bf16");
+  }
+#undef MUIR_MMA
 }
 
 // The eight nibbles of a word as four pairs (nibbles i and i + 4) of numbers
@@ -166,7 +174,11 @@ __global__ void __launch_bounds__(32 * kW4Warps, NB == 1 ? 6 : 3) w4_matvec_kern
   }
   const X* xt[NB];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) xt[b] = x + (n0 + 8 * b + g) * p.K + warp * 128 + 8 * t;
+  for (int b = 0; b < NB; ++b) {
+    // rows past the last repeat it; their results are not stored
+    const int64_t r = n0 + 8 * b + g < p.n ? n0 + 8 * b + g : p.n - 1;
+    xt[b] = x + r * p.K + warp * 128 + 8 * t;
+  }
   for (int kb = warp; kb < blocks; kb += kW4Warps) {
     uint4 w[RT][2];
     __nv_bfloat16 sc[RT][GPB][2];
@@ -186,27 +198,11 @@ __global__ void __launch_bounds__(32 * kW4Warps, NB == 1 ? 6 : 3) w4_matvec_kern
     for (int gr = 0; gr < GPB; ++gr) {
       float part[RT][NB][4];
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) part[rt][b][i] = 0.f;
-#pragma unroll
       for (int jj = 0; jj < 4 / GPB; ++jj) {
         const int j = gr * (4 / GPB) + jj;
         uint32_t xb[NB][XL::PARTS][4];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const int64_t r = n0 + 8 * b + g;
-          if (r < p.n) {
-            XL::get(xt[b] + 32 * j, xb[b]);
-          } else {
-#pragma unroll
-            for (int m = 0; m < XL::PARTS; ++m)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) xb[b][m][i] = 0u;
-          }
-        }
+        for (int b = 0; b < NB; ++b) XL::get(xt[b] + 32 * j, xb[b]);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
           const uint32_t u0 = reinterpret_cast<const uint32_t*>(&w[rt][0])[j], u1 = reinterpret_cast<const uint32_t*>(&w[rt][1])[j];
@@ -218,14 +214,15 @@ __global__ void __launch_bounds__(32 * kW4Warps, NB == 1 ? 6 : 3) w4_matvec_kern
           for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int m = 0; m < XL::PARTS; ++m) {
-              mma_16816<XL::HALF>(part[rt][b], a0, xb[b][m][0], xb[b][m][1]);
-              mma_16816<XL::HALF>(part[rt][b], a1, xb[b][m][2], xb[b][m][3]);
+              if (jj == 0 && m == 0) mma_16816<XL::HALF, true>(part[rt][b], a0, xb[b][m][0], xb[b][m][1]);
+              else mma_16816<XL::HALF, false>(part[rt][b], a0, xb[b][m][0], xb[b][m][1]);
+              mma_16816<XL::HALF, false>(part[rt][b], a1, xb[b][m][2], xb[b][m][3]);
             }
         }
       }
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        const float s0 = kW4Up * __bfloat162float(sc[rt][gr][0]), s1 = kW4Up * __bfloat162float(sc[rt][gr][1]);
+        const float s0 = __bfloat162float(sc[rt][gr][0]), s1 = __bfloat162float(sc[rt][gr][1]);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           acc[rt][b][0] = fmaf(s0, part[rt][b][0], acc[rt][b][0]);
@@ -252,6 +249,7 @@ __global__ void __launch_bounds__(32 * kW4Warps, NB == 1 ? 6 : 3) w4_matvec_kern
       float s = 0.f;
 #pragma unroll
       for (int k = 0; k < kW4Warps; ++k) s += red[k][r >> 3][l][e];
+      s *= kW4Up;
       const int64_t row = n0 + r, col = (tile0 + rt) * 16 + o;
       if (row < p.n && col < p.O) {
         if (p.x_scale) s *= __ldg(p.x_scale + row);
