@@ -67,7 +67,8 @@ def _run(d, t, dtype, lengths, scale, state):
 @pytest.mark.parametrize("case", [
     (1, 1, 1, 32, 32), (2, 1, 3, 128, 128), (1, 31, 2, 64, 32), (1, 33, 1, 128, 64), (3, 127, 2, 32, 128),
     (1, 128, 2, 128, 128), (1, 129, 2, 64, 64), (2, 255, 1, 128, 32), (1, 300, 2, 128, 128), (1, 515, 1, 64, 128),
-    (1, 1025, 1, 32, 64), (1, 640, 2, 128, 128)])
+    (1, 1025, 1, 32, 64), (1, 640, 2, 128, 128),
+    (50, 1, 4, 64, 64), (3, 16, 40, 128, 128), (2, 17, 2, 64, 64), (60, 9, 4, 32, 64)])
 def test_forward_and_gradients(cuda_ok, dtype, case):
     d, t = _make(*case, dtype)
     _run(d, t, dtype, None, 0.125, True)
