@@ -288,6 +288,12 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
   const int pi = blockIdx.y;
   const LinPass p = args.p[pi];  // by value: the waits between uses would reload what a reference names
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid >= 64 && tid < 68) {  // the descriptors, ahead of their first use
+    const int i = tid - 64;
+    if (i < 2 || OUT) {
+      if (i != 3 || p.dc >= 64) tma_prefetch_desc(i == 0 ? &args.b[pi] : i == 1 ? &args.c[pi] : i == 2 ? &args.a[pi] : &args.o[pi]);
+    }
+  }
   const LinUnit u = lin_unit(p);
   const uint32_t base = (smem_u32(lt_sm) + 1023u) & ~1023u;
   // the parts of chunk n's b, given b's own tile
@@ -297,6 +303,19 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
   // third parts of 128 channels go over b, after the scores; of 64 they have room beside the first
   const bool over_b = OUT && PARTS == 3 && p.da > 64;
   auto part3 = [&](int n, uint32_t bt) { return !OUT ? spare + 2u * kLtTile : over_b ? bt : spare + kLtBox; };
+  // chunk n of the walk: its place in the segment
+  auto chunk_at = [&](int n) { return p.reverse ? u.chunks - 1 - n : n; };
+  // tile m of the walk into its slot, in the order b(0) a(0) c(0) b(1) ..
+  const int all_tiles = u.chunks * TILES;
+  auto load_tile = [&](int m) {
+    const int s = m % SLOTS, n = m / TILES, k = m % TILES;
+    const CUtensorMap* map = k == 0 ? &args.b[pi] : k == TILES - 1 ? &args.c[pi] : &args.a[pi];
+    const int d = k == TILES - 1 ? p.dc : p.da, t = (int)(u.t0 + (int64_t)chunk_at(n) * kLtChunk);
+    const uint32_t dst = base + (uint32_t)s * kLtTile;
+    mbar_expect_tx(&full[s], d > 64 ? 2u * kLtBox : kLtBox);
+    tma_load_3d(dst, map, u.h * d, t, u.b, &full[s]);
+    if (d > 64) tma_load_3d(dst + kLtBox, map, u.h * d + 64, t, u.b, &full[s]);
+  };
   if (tid == 0) {
     for (int i = 0; i < SLOTS; ++i) {
       mbar_init(&full[i], 1);
@@ -314,8 +333,12 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
     mbar_init(&b_dsfree[0], 8);
     mbar_init(&b_dsfree[1], 8);
     mbar_init(&b_sready, 8);
+    fence_async_smem();
+    // the first tiles are on their way while the rest of the CTA sets up
+#pragma unroll 1
+    for (int m = 0; m < SLOTS && m < all_tiles; ++m) load_tile(m);
   }
-  if (warp == 0) tmem_alloc(&tslot, 512);
+  if (warp == 1) tmem_alloc(&tslot, 512);
   if (tid < kLtChunk) pw[tid] = exp2f(u.c2 * (float)tid);
   if (tid < 16) pcol[tid] = exp2f(u.c2 * (float)(p.reverse ? tid : 15 - tid));
   tc_fence_before();
@@ -324,30 +347,18 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
   const uint32_t tmem = tslot;
   const uint32_t t_scores = tmem, t_y1 = tmem + 128, t_y2 = tmem + 256;
   auto t_ds = [&](int n) { return tmem + 384u - 128u * (uint32_t)ds_buf(n); };
-  // chunk n of the walk: its place in the segment
-  auto chunk_at = [&](int n) { return p.reverse ? u.chunks - 1 - n : n; };
 
   if (warp < 4) {
     regs_dec<40>();
     if (warp == 0) {
-      // ---- TMA: tiles in the order they are needed, b(n) a(n) c(n) b(n+1) .. --------
+      // ---- TMA: the remaining tiles, each as its slot comes free ------------------------
       if (lane == 0) {
         bool ok = true;
-        int m = 0;
-        auto map_of = [&](int k) { return k == 0 ? &args.b[pi] : k == TILES - 1 ? &args.c[pi] : &args.a[pi]; };
-        auto width = [&](int k) { return k == TILES - 1 ? p.dc : p.da; };
-        auto first = [&](int n) { return (int)(u.t0 + (int64_t)chunk_at(n) * kLtChunk); };
-        for (int n = 0; n < u.chunks && ok; ++n) {
-          for (int k = 0; k < TILES && ok; ++k, ++m) {
-            const int s = m % SLOTS, turn = m / SLOTS;
-            if (turn > 0) ok = lane_wait(&empty[s], (uint32_t)(turn - 1) & 1u);
-            if (!ok) break;
-            const int d = width(k);
-            const uint32_t dst = base + (uint32_t)s * kLtTile;
-            mbar_expect_tx(&full[s], d > 64 ? 2u * kLtBox : kLtBox);
-            for (int x = 0; x < d; x += 64)
-              tma_load_3d(dst + (x ? kLtBox : 0u), map_of(k), u.h * d + x, first(n), u.b, &full[s]);
-          }
+        int m = SLOTS < all_tiles ? SLOTS : all_tiles;
+        for (; m < all_tiles; ++m) {
+          ok = lane_wait(&empty[m % SLOTS], (uint32_t)(m / SLOTS - 1) & 1u);
+          if (!ok) break;
+          load_tile(m);
         }
         // no copy is in flight when the CTA ends, even after a wait that ran out
         for (int s = 0; s < SLOTS; ++s)
@@ -717,7 +728,6 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
         }
       }
     }
-    if (OUT && lane == 0) bulk_wait_all();
     float* dst = nullptr;
     if constexpr (!OUT) dst = p.seg + ((int64_t)u.bh * p.nseg + u.seg) * nstate;
     else if (p.fin && p.nseg == 1) dst = p.fin + (int64_t)u.bh * nstate;
@@ -733,10 +743,11 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
         }
       }
     }
+    if (OUT && lane == 0) bulk_wait_all();
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) tmem_dealloc(tmem, 512);
+  if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace muir
