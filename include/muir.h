@@ -296,8 +296,9 @@ int muir_gate_proj(const void* x, const void* w_down, const void* u_decay, const
  * lengths, where not NULL, gives the valid tokens of each sequence of a padded
  * batch (clamped to [0, T]); tokens behind them are not read, whatever they
  * hold, S_T is the state after the last valid token, and y and the gradients of
- * padded tokens are written as zeros. Outputs must not overlap inputs, but for
- * S_T = S0 below. */
+ * padded tokens are written as zeros. Valid tokens must be finite (a token-token
+ * product is formed for whole runs of up to 128 tokens, and zero times an infinite
+ * value is not zero). Outputs must not overlap inputs, but for S_T = S0 below. */
 typedef struct muir_lin_args {
   int64_t B;      /* sequences */
   int64_t T;      /* tokens per sequence */
