@@ -45,6 +45,7 @@ struct LinPass {
   int64_t T, seglen;
   int B, H, da, dc, nseg;
   int reverse, init_t, seg_t;
+  int exact;  // segment states to fp32 (the final state is made of them), not to 16 bits (they feed bf16 outputs alone)
   float p_scale, o_scale, u_scale;  // of the token-token sum, of the state term, of the state update
 };
 
@@ -127,7 +128,7 @@ __global__ void __launch_bounds__(128) lin_combine_kernel(const __grid_constant_
 // arithmetic at da = dc = 128. Bound by shared-memory reads: the tiles (4 x 4 scores,
 // 2 x 4 outputs and da / 32 x 4 state elements per thread, all read four floats at a
 // time) take about seven products for each 16-byte read. Backward of 2 x 777 tokens, 4
-// heads of 64: 70 us a call, three launches.
+// heads of 64: 55 us a call, three launches.
 constexpr int kLinRun = 64;
 
 constexpr int kLinMaxPasses = 3;

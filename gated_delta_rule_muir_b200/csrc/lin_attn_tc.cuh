@@ -22,15 +22,16 @@
 //
 // A launch that keeps no final state (one of several segments: the final state comes
 // from the segments' own) feeds S only to y, at bf16 accuracy; there b is cut into
-// two parts, 17 bits, by three packed bf16 operations for two elements.
+// two parts, 17 bits, by three packed bf16 operations for two elements. Segment states
+// that no final state is made of leave the third part out as well.
 //
 // Bound: per chunk 128 KB of operands and output, about 5700 cycles at this GPU's
 // copy bandwidth with one CTA per SM; five products of 512 tensor cycles (six with
 // three parts); and shared memory, about 4600 cycles of its 128 bytes a cycle: the
 // products read 2300 cycles' worth (a 128 x 128 x 16 step with both operands in shared
 // memory takes all of it), copies in and out 1000, cutting 770, S and the outputs 500.
-// Measured, one sequence of 32768 tokens, 16 heads of 128: outputs 126 us (83 at the
-// copy bandwidth), the segments' own states 75 (42). With nearly all work on elements
+// Measured, one sequence of 32768 tokens, 16 heads of 128: outputs 124 us (83 at the
+// copy bandwidth), the segments' own states 71 (42). With nearly all work on elements
 // left out of a timing copy the outputs took 105 us, and no single role's work moved
 // them by more than 10: what is left is the traffic and the hand-offs, not one stage.
 // Slower were: masking in unrolled blocks of 32 columns (237 us for both launches
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
   auto part1 = [&](int n, uint32_t bt) { return OUT ? spare : bt; };
   auto part2 = [&](int n, uint32_t bt) { return spare + (OUT ? 1u : (uint32_t)(n & 1)) * kLtTile; };
   // third parts of 128 channels go over b, after the scores; of 64 they have room beside the first
-  const bool over_b = OUT && PARTS == 3 && p.da > 64;
+  const bool thirds = PARTS == 3 && (OUT || p.exact), over_b = OUT && PARTS == 3 && p.da > 64;
   auto part3 = [&](int n, uint32_t bt) { return !OUT ? spare + 2u * kLtTile : over_b ? bt : spare + kLtBox; };
   // chunk n of the walk: its place in the segment
   auto chunk_at = [&](int n) { return p.reverse ? u.chunks - 1 - n : n; };
@@ -394,11 +395,12 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
                (n <= ds_buf(1) || lane_wait(&b_dsfree[ds_buf(n)], ds_phase(n) ^ 1u));
           if (!ok) break;
           tc_fence_after();
-          if constexpr (PARTS == 3) {
+          if (thirds) {
             lt_product<8, false, true, true>(m_ds, part3(n, bt), ct, id_ds);
             if (!OUT) mma_commit(&b_used3);
             lt_product<8, true, true, true>(m_ds, part2(n, bt), ct, id_ds);
           } else {
+            if (!OUT) mma_commit(&b_used3);  // of the chunks before this one
             lt_product<8, false, true, true>(m_ds, part2(n, bt), ct, id_ds);
           }
           lt_product<8, true, true, true>(m_ds, part1(n, bt), ct, id_ds);
@@ -561,7 +563,7 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
           // (columns past da hold other heads' channels: cut as well, rows of dS that nobody reads)
           sts128(l1 + at, make_uint4(p1[0], p1[1], p1[2], p1[3]));
           sts128(l2 + at, make_uint4(p2[0], p2[1], p2[2], p2[3]));
-          if (PARTS == 3) sts128(l3 + at, make_uint4(p3[0], p3[1], p3[2], p3[3]));
+          if (thirds) sts128(l3 + at, make_uint4(p3[0], p3[1], p3[2], p3[3]));
         }
       }
       if (r >= L) {  // c's rows past the last token: zero times anything must stay zero

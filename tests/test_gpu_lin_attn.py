@@ -221,6 +221,22 @@ def test_repeats_streams_and_graphs_agree(cuda_ok, dtype):
         assert all(torch.equal(a, b) for a, b in zip(out, want))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_without_states(cuda_ok, dtype):
+    """No final state and no dS0 wanted: one segment and several."""
+    for T in (200, 2600):
+        d, t = _make(1, T, 2, 64, 128, dtype, seed=12)
+        a = (d["q"], d["k"], d["v"], d["ld"])
+        y, S = muir.lin_attn_fwd(t["q"], t["k"], t["v"], t["ld"], want_state=False)
+        assert S is None
+        _check("y", y, lo.lin_forward(*a)[0], lo.lin_forward_abs(*a)[0], T, dtype)
+        g = muir.lin_attn_bwd(t["q"], t["k"], t["v"], t["ld"], t["dy"], dS_T=t["dS_T"], want_dS0=False)
+        assert g["dS0"] is None
+        gr, gA = lo.lin_backward(*a, d["dy"], dS_T=d["dS_T"]), lo.lin_backward_abs(*a, d["dy"], dS_T=d["dS_T"])
+        for n in ("dq", "dk", "dv"):
+            _check(n, g[n], gr[n], gA[n], T, dtype)
+
+
 def test_dS0_keeps_its_own_buffer(cuda_ok):
     d, t = _make(1, 64, 2, 64, 64, torch.bfloat16)
     for n in ("S0", "dS_T"):
