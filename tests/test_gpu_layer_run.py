@@ -106,3 +106,35 @@ def test_training_gradients_chain(cuda_ok):
     diff = (loss(up) - loss(down)) / (2 * step)
     size = (y.double().abs() * dy.double().abs()).sum().item()
     assert abs(diff - (dx.double().view_as(real) * real).sum().item()) <= 64 * size * step ** 2 / 6 + 2.0 ** -18 * size / step
+
+
+def test_two_calls_at_once(cuda_ok):
+    """Calls on two streams, interleaved: each as it is alone."""
+    def work(seed, stream):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        q, k, v, dy = (torch.randn(2, 900, 3, 64, generator=g, device="cuda").bfloat16() for _ in range(4))
+        ld = -torch.rand(3, generator=g, device="cuda")
+        x, w = torch.randn(64, 512, generator=g, device="cuda"), torch.randn(512, generator=g, device="cuda")
+        codes = torch.randint(0, 16, (300, 512), generator=g, device="cuda", dtype=torch.uint8)
+        packed = muir.w4_pack(codes, torch.rand(300, 8, generator=g, device="cuda").bfloat16())
+        torch.cuda.synchronize()
+
+        def call():
+            y, S = muir.lin_attn_fwd(q, k, v, ld, stream=stream)
+            gr = muir.lin_attn_bwd(q, k, v, ld, dy, stream=stream)
+            f = muir.rms_norm(x, w, stream=stream)
+            dx, dw = muir.rms_norm_bwd(x, x, w, f["rstd"], stream=stream)
+            return [y, S, *gr.values(), f["y"], dx, dw, muir.w4_matvec(f["y"], *packed, 300, stream=stream)]
+        return call
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    calls = [work(i, s) for i, s in enumerate(streams)]
+    alone = []
+    for c in calls:
+        alone.append(c())
+        torch.cuda.synchronize()
+    for _ in range(5):
+        both = [c() for c in calls]
+    torch.cuda.synchronize()
+    for a, b in zip(alone, both):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert muir.device_status() == 0
