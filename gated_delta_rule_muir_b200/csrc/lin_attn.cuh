@@ -68,6 +68,11 @@ __device__ __forceinline__ LinDecay lin_decay(float c2, int64_t L) {
   const float x = c2 * (float)L, w = exp2f(x);
   return w > 0.5f ? LinDecay{1.f, expm1f(x * 0.6931471805599453f)} : LinDecay{w, 0.f};
 }
+// of one token, from log lambda
+__device__ __forceinline__ LinDecay lin_decay1(float log_decay) {
+  const float e = expm1f(log_decay);
+  return e > -0.5f ? LinDecay{1.f, e} : LinDecay{expf(log_decay), 0.f};
+}
 
 __device__ __forceinline__ int64_t lin_length(const LinPass& p, int b) {
   if (!p.lengths) return p.T;
@@ -331,7 +336,9 @@ __global__ void __launch_bounds__(256) lin_simt_kernel(const __grid_constant__ L
 
 // ---- one token ------------------------------------------------------------------
 //
-// y_j = scale (lambda sum_i q_i S_ij + (q . k) v_j), S_ij <- lambda S_ij + k_i v_j.
+// S_ij <- lambda S_ij + k_i v_j, y_j = scale sum_i q_i S_ij of the new state. The decay
+// is applied as in LinDecay, for the same reason: lambda rounded to fp32 would be off by
+// the same 2^-25 at every token of a stream.
 // Memory bound: one CTA per (sequence, head, 32 columns) reads its slab of the
 // state once into registers and writes it once, as the gated-delta-rule step does
 // (1536 sequences x 16 heads of 128 x 128: 475 us, 6.8 TB/s).
@@ -351,7 +358,7 @@ __global__ void __launch_bounds__(128) lin_step_kernel(LinStepParams p) {
   const int slabs = p.dv >> 5;
   const int slab = (int)(blockIdx.x % slabs);
   const int64_t nh = blockIdx.x / slabs;
-  __shared__ float s_k[DK], s_q[DK], s_red[4][32], s_dot[4];
+  __shared__ float s_k[DK], s_q[DK], s_red[4][32];
 
   float* Sb = p.S + nh * DK * (int64_t)p.dv + slab * 32 + cg * 4;
   float4 x[RM];
@@ -360,28 +367,20 @@ __global__ void __launch_bounds__(128) lin_step_kernel(LinStepParams p) {
   float vj[4];
   const int64_t co = nh * p.dv + slab * 32 + cg * 4;
   Elt<T>::ld4(static_cast<const T*>(p.v) + co, vj);
-  float kq = 0.f;
   if (tid < DK) {
-    const float kk = Elt<T>::ld(static_cast<const T*>(p.k) + nh * DK + tid);
-    const float qq = Elt<T>::ld(static_cast<const T*>(p.q) + nh * DK + tid);
-    s_k[tid] = kk;
-    s_q[tid] = qq;
-    kq = kk * qq;
+    s_k[tid] = Elt<T>::ld(static_cast<const T*>(p.k) + nh * DK + tid);
+    s_q[tid] = Elt<T>::ld(static_cast<const T*>(p.q) + nh * DK + tid);
   }
-  const float lam = expf(__ldg(p.log_decay + (int)(nh % p.H)));
-  kq = warp_sum(kq);
-  if ((tid & 31) == 0) s_dot[tid >> 5] = kq;
+  const LinDecay w = lin_decay1(__ldg(p.log_decay + (int)(nh % p.H)));
   __syncthreads();
   float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int m = 0; m < RM; ++m) {
     const int i = rg + 16 * m;
     const float kk = s_k[i], qq = s_q[i];
-    x[m].x *= lam; x[m].y *= lam; x[m].z *= lam; x[m].w *= lam;
+    x[m] = make_float4(w(x[m].x, kk * vj[0]), w(x[m].y, kk * vj[1]), w(x[m].z, kk * vj[2]), w(x[m].w, kk * vj[3]));
     o[0] = fmaf(qq, x[m].x, o[0]); o[1] = fmaf(qq, x[m].y, o[1]);
     o[2] = fmaf(qq, x[m].z, o[2]); o[3] = fmaf(qq, x[m].w, o[3]);
-    x[m].x = fmaf(kk, vj[0], x[m].x); x[m].y = fmaf(kk, vj[1], x[m].y);
-    x[m].z = fmaf(kk, vj[2], x[m].z); x[m].w = fmaf(kk, vj[3], x[m].w);
     *reinterpret_cast<float4*>(Sb + (int64_t)i * p.dv) = x[m];
   }
 #pragma unroll
@@ -396,12 +395,11 @@ __global__ void __launch_bounds__(128) lin_step_kernel(LinStepParams p) {
   }
   __syncthreads();
   if (tid < 8) {
-    const float KQ = s_dot[0] + s_dot[1] + s_dot[2] + s_dot[3];
     float yo[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int jj = cg * 4 + c;
-      yo[c] = p.scale * fmaf(KQ, vj[c], s_red[0][jj] + s_red[1][jj] + s_red[2][jj] + s_red[3][jj]);
+      yo[c] = p.scale * (s_red[0][jj] + s_red[1][jj] + s_red[2][jj] + s_red[3][jj]);
     }
     Elt<T>::st4(static_cast<T*>(p.y) + co, yo);
   }
