@@ -1,7 +1,7 @@
 // Root-mean-square norm of token rows, with the residual's addition.
 //
 //   h = x + residual                         (h = x without a residual)
-//   rstd = (mean_d h_d^2 + eps)^(-1/2)
+//   rstd = (mean_d h_d^2 + eps)^(-1/2)       (0 for a row of zeros without an eps)
 //   y_d = h_d rstd weight_d
 //
 // y in the input's type, or in 8 bits: with top = max_d |y_d|, scale = top / 448
@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(NT > 32 ? NT : 256) rms_norm_kernel(NormParams
     for (int i = 0; i < 8; ++i) ss = fmaf(x[v][i], x[v][i], ss);
   }
   ss = row_sum<NT>(ss, slot[0]);
-  const float rstd = 1.f / sqrtf(ss / (float)p.d + p.eps);
+  const float ms = ss / (float)p.d + p.eps;
+  const float rstd = ms == 0.f ? 0.f : 1.f / sqrtf(ms);
   if (lane == 0 && p.rstd) p.rstd[row] = rstd;
   float top = 0.f;
 #pragma unroll
