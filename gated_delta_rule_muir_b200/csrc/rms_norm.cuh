@@ -8,7 +8,8 @@
 // (448 is e4m3's largest number) and q_d = e4m3(y_d 448 / top), so that
 // q_d scale ~ y_d; a row of zeros has scale 0 and codes 0. The norm is taken of
 // the fp32 sum; the residual stream h that is written out is rounded once, to the
-// input's type. Statistics are fp32.
+// input's type. Statistics are fp32; rows whose squares leave fp32's range are scaled by
+// a power of two first.
 //
 // Backward, with xh = h rstd and g = dy weight:
 //   dx_d = rstd (g_d - xh_d mean_d(g xh)) + dh_d      dweight_d = sum_rows dy_d xh_d
@@ -117,7 +118,35 @@ __global__ void __launch_bounds__(NT > 32 ? NT : 256) rms_norm_kernel(NormParams
   }
   ss = row_sum<NT>(ss, slot[0]);
   const float ms = ss / (float)p.d + p.eps;
-  const float rstd = ms == 0.f ? 0.f : 1.f / sqrtf(ms);
+  float rs = ms == 0.f ? 0.f : 1.f / sqrtf(ms), rstd = rs;  // y = x rs w with x as it stands in the registers
+  if (isinf(ss) || ms < 0x1p-100f) {
+    // squares outside fp32's range (the whole row comes here or no thread of it): once
+    // more with the row brought near 1 by a power of two. eps counts for the size as well,
+    // so that neither term overflows. An infinity in the row stays one.
+    float big = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) big = max_nan(big, fabsf(x[v][i]));
+    big = row_max<NT>(big, slot[1]);
+    if (!isinf(big)) {
+      const float top = fmaxf(big, sqrtf(p.eps));
+      const int e = top > 0.f ? max(-126, min(126, -ilogbf(top))) : 0;
+      const float up = ldexpf(1.f, e);
+      ss = 0.f;
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[v][i] *= up;
+          ss = fmaf(x[v][i], x[v][i], ss);
+        }
+      ss = row_sum<NT>(ss, slot[0]);
+      const float m = ss / (float)p.d + p.eps * up * up;
+      rs = m == 0.f ? 0.f : 1.f / sqrtf(m);
+      rstd = rs * up;
+    }
+  }
   if (lane == 0 && p.rstd) p.rstd[row] = rstd;
   float top = 0.f;
 #pragma unroll
@@ -128,7 +157,7 @@ __global__ void __launch_bounds__(NT > 32 ? NT : 256) rms_norm_kernel(NormParams
       Elt<float>::ld8(p.weight + e, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        x[v][i] = x[v][i] * rstd * w[i];
+        x[v][i] = x[v][i] * rs * w[i];
         top = max_nan(top, fabsf(x[v][i]));
       }
       if constexpr (!QUANT) Elt<T>::st8(static_cast<T*>(p.y) + off + e, x[v]);

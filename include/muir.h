@@ -360,7 +360,9 @@ int muir_lin_step(const muir_lin_step_args* a, void* stream);
  * fp32 and the norm is taken of the unrounded sum. h is required with a residual
  * and ignored without one; it may be the residual's buffer or x's, and y may be x's.
  * rstd [n] may be NULL. d: a multiple of 8 up to 16384; n >= 0; eps >= 0. A row of
- * zeros gives y = 0, with eps = 0 too: its rstd is then 0.
+ * zeros gives y = 0, with eps = 0 too: its rstd is then 0. Rows of any finite size are
+ * normed (squares may lie outside fp32's range); only rstd itself is infinite where it
+ * is above fp32's largest number (subnormal rows without an eps).
  * muir_rms_norm_quant writes the norm in 8 bits (e4m3) instead, with a scale per
  * row: scale = max_d |y| / 448 and q the nearest e4m3 number to y / scale, so that
  * q scale ~ y; a row of zeros has scale 0 and q 0. */
