@@ -263,7 +263,6 @@ int muir_lin_fwd(const muir_lin_args* a, void* y, float* S_T, void* ws, size_t w
   p.out = y;
   p.init = a->S0;
   p.fin = S_T;
-  p.exact = S_T != nullptr;
   p.seg = need ? static_cast<float*>(ws) : nullptr;
   p.p_scale = p.o_scale = a->scale;
   p.u_scale = 1.f;
@@ -309,7 +308,6 @@ int muir_lin_bwd(const muir_lin_args* a, const muir_lin_grads* g, void* ws, size
   p[0].out = g->dv;
   p[0].init = g->dS_T;
   p[0].fin = g->dS0;
-  p[0].exact = g->dS0 != nullptr;
   p[0].seg = dS;
   p[0].reverse = 1;
   p[0].p_scale = p[0].u_scale = a->scale;

@@ -45,7 +45,6 @@ struct LinPass {
   int64_t T, seglen;
   int B, H, da, dc, nseg;
   int reverse, init_t, seg_t;
-  int exact;  // segment states to fp32 (the final state is made of them), not to 16 bits (they feed bf16 outputs alone)
   float p_scale, o_scale, u_scale;  // of the token-token sum, of the state term, of the state update
 };
 

@@ -293,6 +293,14 @@ int muir_gate_proj(const void* x, const void* w_down, const void* u_decay, const
  * gradient. Layouts and dtypes as for muir_chunk_fwd; dk, dv in {32, 64, 128}; any
  * T >= 0 (no padding to a chunk is needed), B H <= 65535, T <= 2^30.
  *
+ * fp32 operands are multiplied as they are. bf16 operands go to the tensor cores: the
+ * weight of each pair of tokens (q_t . k_s with its decay; in the gradients likewise) and
+ * the state that y and the gradients read are rounded once to bf16 as operands (2^-8 of
+ * the sum of absolute terms at most, in all; one head of 32 channels excepted), beside the
+ * rounding of the output itself. The state they read may take its writes from operands
+ * cut to 1.5 2^-15; S_T, dS0 and the states carried over long sequences never do: those are
+ * fp32 sums of exact products. Where that is too coarse, pass fp32 operands.
+ *
  * lengths, where not NULL, gives the valid tokens of each sequence of a padded
  * batch (clamped to [0, T]); tokens behind them are not read, whatever they
  * hold, S_T is the state after the last valid token, and y and the gradients of
