@@ -54,14 +54,11 @@ struct LinPlan {
 
 // bf16 operands go to the tensor cores, fp32 ones to the CUDA cores (one bf16
 // rounding of the weights would be all of fp32's accuracy). A box of the copies
-// covers 64 channels, so a token row has at least that many. A few tokens of a few
-// heads, no more than one CTA for each SM, stay on the CUDA cores: as fast (16 heads of
-// 64, 16 tokens: forward 10.3 against 10.0 us, backward 10.7 against 10.2; of 128,
-// forward 16.0 against 14.5) and without the roundings of the weights and the state.
-bool lin_use_tc(const muir_lin_args* a, int outs) {
-  const int wide = outs > 1 && a->dk > a->dv ? a->dk : a->dv;  // columns of the widest pass
-  const int64_t ctas = a->B * a->H * (wide / 32) * outs;
-  if (a->T <= 16 && ctas <= kSMs) return false;
+// covers 64 channels, so a token row has at least that many. Few tokens are no
+// exception, so that a short sequence's result is the same in every batch; they are no
+// faster on the CUDA cores (in a graph, forward of 16 tokens, 16 heads of 64: 8.6 us on
+// the CUDA cores, 8.5 on the tensor cores; of 128, 12.9 and 11.2; one token of 64, 8.1 and 8.5).
+bool lin_use_tc(const muir_lin_args* a) {
   return a->dtype == MUIR_BF16 && a->T > 0 && (int64_t)a->H * a->dk >= 64 && (int64_t)a->H * a->dv >= 64;
 }
 
@@ -78,7 +75,7 @@ bool lin_use_tc(const muir_lin_args* a, int outs) {
 // CUDA cores: as many CTAs as fit beside one another, three for each SM up to 64
 // channels and two for 128.
 LinPlan lin_plan(const muir_lin_args* a, int outs, int states) {
-  LinPlan pl{lin_use_tc(a, outs), 1, 0};
+  LinPlan pl{lin_use_tc(a), 1, 0};
   const int64_t run = pl.tc ? muir::kLtChunk : muir::kLinRun;
   const int64_t runs = a->T > 0 ? (a->T + run - 1) / run : 1;
   int64_t n = 1;
