@@ -452,8 +452,9 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
     // 16 columns at a time in one short loop (an unrolled body of this size runs at the
     // pace of instruction fetches). lambda^gap = (row factor) (column factor), the
     // column factor at most 1 and the row factor at most lambda^-15, 2^60 for decays
-    // above 2^-4; below that the powers are taken from the table one by one.
-    const bool mild = u.c2 > -4.f;
+    // above 2^-4; below that, and for scales above 2^60, which would take the row factor
+    // out of range, the powers are taken from the table one by one.
+    const bool mild = u.c2 > -4.f && fabsf(p.p_scale) <= 0x1p60f;
     bool ok = true;
     for (int n = 0; n < u.chunks && ok; ++n) {
       const uint32_t ph = (uint32_t)n & 1u;
