@@ -44,6 +44,12 @@ def _dims(t, name, n):
     return t.shape
 
 
+def _int32(name, size):
+    """Sizes that the C ABI holds in 32 bits: a larger one would reach it cut to its low bits."""
+    if size > 0x7fffffff:
+        raise ValueError(f"{name} must be below 2^31, got {size}")
+
+
 def _io_code(t, name):
     code = {torch.float32: N.MUIR_F32, torch.bfloat16: N.MUIR_BF16}.get(t.dtype)
     if code is None:
@@ -104,6 +110,7 @@ def _out(t, name, shape, dtype, device):
 def _lin_args(q, k, v, log_decay, scale, lengths, S0):
     B, T, H, dk = _dims(q, "q", 4)
     dv = _dims(v, "v", 4)[3]
+    _int32("a number of heads or channels", max(H, dk, dv))
     dev = q.device
     code = _io_code(q, "q")
     _need(q, "q", (B, T, H, dk), q.dtype, dev)
@@ -171,6 +178,7 @@ def lin_attn_step(S, q, k, v, log_decay, *, scale=1.0, y=None, stream=None):
     """One token of lin_attn_fwd for n sequences: S [n,H,dk,dv] fp32 updated in place, q, k
     [n,H,dk], v [n,H,dv]. Returns y [n,H,dv]."""
     n, H, dk, dv = _dims(S, "S", 4)
+    _int32("a number of heads or channels", max(H, dk, dv))
     dev = S.device
     code = _io_code(q, "q")
     _need(S, "S", (n, H, dk, dv), torch.float32, dev)
@@ -187,6 +195,7 @@ def lin_attn_step(S, q, k, v, log_decay, *, scale=1.0, y=None, stream=None):
 
 def _norm_operands(x, weight, residual):
     n, d = _dims(x, "x", 2)
+    _int32("d", d)
     dev = x.device
     code = _io_code(x, "x")
     _need(x, "x", (n, d), x.dtype, dev)
@@ -232,6 +241,7 @@ def rms_norm_bwd(dy, h, weight, rstd, *, dh=None, dx=None, dweight=None, workspa
     """Gradients of rms_norm from its h (its x, without a residual) and rstd: (dx [n,d], dweight
     [d] fp32). dx is the gradient of x and of the residual alike; dh is the cotangent of h."""
     n, d = _dims(h, "h", 2)
+    _int32("d", d)
     dev = h.device
     code = _io_code(h, "h")
     _need(h, "h", (n, d), h.dtype, dev)
@@ -255,6 +265,7 @@ def w4_quantize(w, *, group=128, stream=None):
     """Weights [O,K] (fp32 or bf16) to 4 bits: (codes [O,K] uint8 in 0..15, scales [O,K/group]
     bf16), w ~ scale (code - 8), scale = max |w| / 7 of each group."""
     O, K = _dims(w, "w", 2)
+    _int32("O and K", max(O, K))
     dev = w.device
     code = _io_code(w, "w")
     _need(w, "w", (O, K), w.dtype, dev)
@@ -272,6 +283,7 @@ def w4_pack(codes, scales, *, stream=None):
     """Codes [O,K] uint8 and scales [O,K/group] bf16 in the layout of w4_matvec: (wq uint8
     [ceil(O/16), K/128, 1024], ws bf16 [ceil(O/16), K/128, 128/group, 16]); see include/muir.h."""
     O, K = _dims(codes, "codes", 2)
+    _int32("O and K", max(O, K))
     ng = _dims(scales, "scales", 2)[1]
     dev = codes.device
     if K % 128 or ng == 0 or K % ng or K // ng not in (32, 64, 128):
@@ -293,6 +305,7 @@ def w4_matvec(x, wq, ws, O, *, x_scale=None, out_dtype=None, y=None, stream=None
     fp32 or bf16 (y of the same type), or float8_e4m3fn with x_scale [n] fp32, as rms_norm_quant
     gives them (y bf16, or fp32 by out_dtype). Meant for few rows: weights are read once per 32."""
     n, K = _dims(x, "x", 2)
+    _int32("O and K", max(O, K))
     dev = x.device
     tiles, blocks, _ = _dims(wq, "wq", 3)
     gpb = _dims(ws, "ws", 4)[2]
