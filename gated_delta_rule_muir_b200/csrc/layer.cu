@@ -510,6 +510,7 @@ namespace {
 int w4_validate(const char* who, int32_t K, int32_t O, int32_t group) {
   if (K <= 0 || K % 128 || O <= 0)
     return fail(MUIR_ERR_UNSUPPORTED, "%s: K must be a multiple of 128 and O positive (got %d, %d)", who, K, O);
+  if (O > kMaxBlocks - 15) return fail(MUIR_ERR_UNSUPPORTED, "%s: O must be at most 2^31 - 16", who);  // whole tiles, in 32 bits
   if (group != 32 && group != 64 && group != 128) return fail(MUIR_ERR_UNSUPPORTED, "%s: group %d", who, group);
   return MUIR_OK;
 }

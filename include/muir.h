@@ -390,7 +390,7 @@ int muir_rms_norm_bwd(const void* dy, const void* h, const float* weight, const 
 /* Product of a few rows with 4-bit weights and group scales, the projections of a
  * decode step:
  *     y[n][o] = x_scale[n] sum_k x[n][k] scale[o][k / group] (code[o][k] - 8)
- * K a multiple of 128, group 32, 64 or 128, any O > 0 and n >= 0 (weights are read
+ * K a multiple of 128, group 32, 64 or 128, 0 < O <= 2^31 - 16 and n >= 0 (weights are read
  * once per 32 rows). x [n][K]: MUIR_F32 or MUIR_BF16 with y of the same type, or
  * MUIR_E4M3 with y of either type and x_scale [n] (NULL: 1). Sums are fp32.
  *

@@ -1,10 +1,14 @@
 """Sizes past 32 bits are refused before they reach the C ABI, which holds them in 32
-bits (on meta tensors: nothing is allocated, nothing reaches the GPU)."""
+bits (on meta tensors and fake addresses: nothing is allocated, nothing reaches the GPU)."""
+import ctypes as C
+
 import pytest
 import torch
 
 import gated_delta_rule_muir_b200 as muir
+from gated_delta_rule_muir_b200 import _native as N
 
+FAKE = C.c_void_p(1 << 20)
 BIG = 1 << 32
 
 
@@ -32,3 +36,17 @@ def _m(*shape, dtype=torch.float32):
 def test_the_binding_refuses_sizes_past_32_bits(call):
     with pytest.raises(ValueError, match="2\\^31"):
         call()
+
+
+def test_outputs_that_do_not_fill_whole_tiles_below_32_bits():
+    from gated_delta_rule_muir_b200 import build
+    build.build()
+    lib = N.load()
+    top = (1 << 31) - 1
+    sb = C.c_size_t(0)
+    assert lib.muir_w4_bytes(128, top - 15, 128, C.byref(sb)) == (top - 15) * 64
+    for O in (top - 14, top):
+        assert lib.muir_w4_bytes(128, O, 128, C.byref(sb)) == 0
+        assert lib.muir_w4_quantize(FAKE, FAKE, FAKE, 128, O, 128, N.MUIR_F32, None) == N.MUIR_ERR_UNSUPPORTED
+        assert lib.muir_w4_pack(FAKE, FAKE, FAKE, FAKE, 128, O, 128, None) == N.MUIR_ERR_UNSUPPORTED
+        assert lib.muir_w4_matvec(FAKE, None, FAKE, FAKE, FAKE, 1, 128, O, 128, N.MUIR_BF16, N.MUIR_BF16, None) == N.MUIR_ERR_UNSUPPORTED
