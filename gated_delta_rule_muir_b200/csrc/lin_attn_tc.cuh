@@ -524,9 +524,11 @@ __global__ void __launch_bounds__(kLtThreads, 1) lin_tc_kernel(const __grid_cons
       const uint32_t line = bt + place, l1 = part1(n, bt) + place, l2 = part2(n, bt) + place, l3 = part3(n, bt) + place;
       const float wt = r < L ? p.u_scale * exp2f(u.c2 * (float)(p.reverse ? r + 1 : L - 1 - r)) : 0.f;
       ok = warp_wait(&full[mb % SLOTS], (uint32_t)(mb / SLOTS) & 1u);
-      if (L < kLtChunk) ok = ok && warp_wait(&full[mc % SLOTS], (uint32_t)(mc / SLOTS) & 1u);
       // the tiles of the last parts have been used; before third parts go over b, the scores have been formed
       if (n > 0) ok = ok && warp_wait(OUT ? &b_ds[0] : &b_used3, (uint32_t)(n - 1) & 1u);
+      // c only after that: the last parts came behind the scores of their chunk, so the tile
+      // before c's in its slot (a's of that chunk) has landed, and a parity names one phase
+      if (L < kLtChunk) ok = ok && warp_wait(&full[mc % SLOTS], (uint32_t)(mc / SLOTS) & 1u);
       if (over_b) ok = ok && warp_wait(&b_scores, (uint32_t)n & 1u);
       if (!ok) break;
       // packed bf16, two parts: with the weight as w1 + w2, p1 = b w1 rounded, and
