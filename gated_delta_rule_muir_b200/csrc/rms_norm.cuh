@@ -76,9 +76,10 @@ __device__ __forceinline__ float row_max(float x, float* slot) {
 }
 
 // NT threads per row, V pieces of 8 elements per thread: piece (v, thread) holds
-// elements 8 (v NT + thread) .. + 7, absent past d.
+// elements 8 (v NT + thread) .. + 7, absent past d. (Two CTAs asked for where 32 floats
+// a thread otherwise spill for a third one: 32768 x 1024 fp32, 85 us against 89; elsewhere the compiler's choice.)
 template <typename T, int NT, int V, bool QUANT>
-__global__ void __launch_bounds__(NT > 32 ? NT : 256) rms_norm_kernel(NormParams p) {
+__global__ void __launch_bounds__(NT > 32 ? NT : 256, NT == 32 && V == 4 && sizeof(T) == 4 ? 2 : 0) rms_norm_kernel(NormParams p) {
   __shared__ float slot[2][32];
   constexpr int ROWS = NT > 32 ? 1 : 8;
   const int lane = NT > 32 ? threadIdx.x : threadIdx.x & 31;
@@ -117,9 +118,8 @@ __global__ void __launch_bounds__(NT > 32 ? NT : 256) rms_norm_kernel(NormParams
     for (int i = 0; i < 8; ++i) ss = fmaf(x[v][i], x[v][i], ss);
   }
   ss = row_sum<NT>(ss, slot[0]);
-  const float ms = ss / (float)p.d + p.eps;
-  float rs = ms == 0.f ? 0.f : 1.f / sqrtf(ms), rstd = rs;  // y = x rs w with x as it stands in the registers
-  if (isinf(ss) || ms < 0x1p-100f) {
+  float ms = ss / (float)p.d + p.eps, up = 1.f;
+  if (isinf(ss) || (ss < 0x1p-86f && p.eps < 0x1p-100f)) {
     // squares outside fp32's range (the whole row comes here or no thread of it): once
     // more with the row brought near 1 by a power of two. eps counts for the size as well,
     // so that neither term overflows. An infinity in the row stays one.
@@ -127,12 +127,12 @@ __global__ void __launch_bounds__(NT > 32 ? NT : 256) rms_norm_kernel(NormParams
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) big = max_nan(big, fabsf(x[v][i]));
+      for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(x[v][i]));
     big = row_max<NT>(big, slot[1]);
     if (!isinf(big)) {
-      const float top = fmaxf(big, sqrtf(p.eps));
-      const int e = top > 0.f ? max(-126, min(126, -ilogbf(top))) : 0;
-      const float up = ldexpf(1.f, e);
+      // exponents by their bits (0 for zeros and subnormal numbers), of eps that of its root
+      const int e = (int)(__float_as_uint(big) >> 23), er = p.eps > 0.f ? ((int)(__float_as_uint(p.eps) >> 23) + 127) >> 1 : 0;
+      up = __uint_as_float((uint32_t)(254 - max(1, min(253, max(e, er)))) << 23);
       ss = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v)
@@ -141,13 +141,11 @@ __global__ void __launch_bounds__(NT > 32 ? NT : 256) rms_norm_kernel(NormParams
           x[v][i] *= up;
           ss = fmaf(x[v][i], x[v][i], ss);
         }
-      ss = row_sum<NT>(ss, slot[0]);
-      const float m = ss / (float)p.d + p.eps * up * up;
-      rs = m == 0.f ? 0.f : 1.f / sqrtf(m);
-      rstd = rs * up;
+      ms = row_sum<NT>(ss, slot[0]) / (float)p.d + p.eps * up * up;
     }
   }
-  if (lane == 0 && p.rstd) p.rstd[row] = rstd;
+  const float rs = ms == 0.f ? 0.f : 1.f / sqrtf(ms);  // rstd = rs up; y = x rs w, x being up times the row's
+  if (lane == 0 && p.rstd) p.rstd[row] = rs * up;
   float top = 0.f;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
