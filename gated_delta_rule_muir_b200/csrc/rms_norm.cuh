@@ -80,7 +80,7 @@ __device__ __forceinline__ float row_max(float x, float* slot) {
 // a thread otherwise spill for a third one: 32768 x 1024 fp32, 85 us against 89; elsewhere the compiler's choice.)
 template <typename T, int NT, int V, bool QUANT>
 __global__ void __launch_bounds__(NT > 32 ? NT : 256, NT == 32 && V == 4 && sizeof(T) == 4 ? 2 : 0) rms_norm_kernel(NormParams p) {
-  __shared__ float slot[2][32];
+  __shared__ float slot[3][32];  // sums, the largest y, the largest x: a reduction's slot is only written behind a later one's barrier
   constexpr int ROWS = NT > 32 ? 1 : 8;
   const int lane = NT > 32 ? threadIdx.x : threadIdx.x & 31;
   const int64_t row = (int64_t)blockIdx.x * ROWS + (NT > 32 ? 0 : threadIdx.x >> 5);
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(NT > 32 ? NT : 256, NT == 32 && V == 4 && size
     for (int v = 0; v < V; ++v)
 #pragma unroll
       for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(x[v][i]));
-    big = row_max<NT>(big, slot[1]);
+    big = row_max<NT>(big, slot[2]);
     if (!isinf(big)) {
       // exponents by their bits (0 for zeros and subnormal numbers), of eps that of its root
       const int e = (int)(__float_as_uint(big) >> 23), er = p.eps > 0.f ? ((int)(__float_as_uint(p.eps) >> 23) + 127) >> 1 : 0;

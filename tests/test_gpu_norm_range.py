@@ -94,3 +94,19 @@ def test_subnormal_rows(cuda_ok):
     y, _, _ = lo.rms_norm(_np(x), _np(w), eps=0.0)
     assert (np.abs(_np(o["y"]) - y) <= 32 * U * np.abs(y)).all()
     assert o["rstd"].item() == float("inf")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("dim", [2048, 4104, 16384])
+def test_rows_with_infinities_in_8_bits_again_and_again(cuda_ok, dtype, dim):
+    """Every other row holds an infinity: no row of any call differs from the first call's."""
+    x, w = _make(64, dim, dtype, 4)
+    x[::2, dim // 3] = float("inf")
+    first = muir.rms_norm_quant(x, w)
+    assert first["scale"][::2].isnan().all() and first["scale"][1::2].isfinite().all() and (first["rstd"][::2] == 0).all()
+    bits = {m: first[m].view(torch.uint8) for m in first}
+    differing = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(300):
+        o = muir.rms_norm_quant(x, w)
+        differing += sum((o[m].view(torch.uint8) != bits[m]).sum() for m in bits)
+    assert differing.item() == 0
