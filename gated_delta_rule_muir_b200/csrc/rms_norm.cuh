@@ -19,9 +19,9 @@
 // Memory bound: every row is read once, kept in registers across its reduction
 // and written once. Rows up to 1024 wide take a warp each (eight rows per CTA, no
 // barrier); wider rows take one CTA. Measured: 32768 x 2048 bf16 with the residual
-// 84 us (6.4 TB/s, 99% of the copy rate); backward of 8191 x 2048 bf16 28 us and 4 us
-// for the column sums (4.2 TB/s together; 42 us before the next row's loads were issued
-// ahead of a row's reduction).
+// 83 us (6.5 TB/s, the copy rate), to 8 bits of 131072 x 512 73 us; backward of 8191 x 2048
+// bf16 28 us and 4 us for the column sums (4.2 TB/s together; 42 us before the next row's
+// loads were issued ahead of a row's reduction).
 #pragma once
 
 #include <cuda_fp8.h>

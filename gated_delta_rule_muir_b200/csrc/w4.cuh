@@ -5,9 +5,11 @@
 // Weights are read once per 32 rows of x, which bounds the product for the few
 // rows of a decode step: O K / 2 bytes and 2 O K / group bytes of scales. Measured
 // (K = 2048): 50257 outputs, eight e4m3 rows, groups of 64: 17.4 us, 3.2 TB/s; 6144
-// outputs, one bf16 row: 3.8 us a call in a graph. The rest of the wide product's time
-// is the integer work of turning codes into numbers (seven operations for eight codes)
-// and the inputs, fetched again by every CTA.
+// outputs, one bf16 row: 3.8 us a call in a graph. The wide product is half as fast as
+// its bytes: a warp executes 21 instructions for each word of eight codes, of which 9
+// turn the codes into numbers and 12 are the inputs (fetched and converted again by every
+// CTA), two-byte scales, products and addresses, and no loads of the next block are in
+// flight while a block is multiplied.
 //
 // Layout. Tiles of 16 outputs x 128 inputs, 1024 bytes each, so that a warp
 // reads a tile as two coalesced 16-byte loads per lane and finds in its registers

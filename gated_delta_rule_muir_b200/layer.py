@@ -141,7 +141,8 @@ def lin_attn_fwd(q, k, v, log_decay, *, scale=1.0, lengths=None, S0=None, want_s
     log_decay [H] fp32 (<= 0), lengths [B] int32 (valid tokens of a padded batch), S0
     [B,H,dk,dv] fp32. Returns (y [B,T,H,dv], S_T [B,H,dk,dv] fp32 or None); y is zero at padded
     tokens and S_T is the state after the last valid one. The decays are constants: they get
-    no gradient."""
+    no gradient. bf16 operands are multiplied on the tensor cores, with one bf16 rounding of
+    the token-token weights and of the state that y reads; fp32 operands at fp32 accuracy."""
     a, (B, T, H, dk, dv, dt, dev) = _lin_args(q, k, v, log_decay, scale, lengths, S0)
     lib = N.load()
     y = _like(y, "y", v)
