@@ -57,7 +57,8 @@ struct LinPlan {
 // covers 64 channels, so a token row has at least that many. Few tokens are no
 // exception, so that a short sequence's result is the same in every batch; they are no
 // faster on the CUDA cores (in a graph, forward of 16 tokens, 16 heads of 64: 8.6 us on
-// the CUDA cores, 8.5 on the tensor cores; of 128, 12.9 and 11.2; one token of 64, 8.1 and 8.5).
+// the CUDA cores, 8.5 on the tensor cores; of 128, 12.9 and 11.2; one token of 64, 8.1 and
+// 8.5; a call outside a graph encodes four tensor maps for it, 14.9 and 15.4 us).
 bool lin_use_tc(const muir_lin_args* a) {
   return a->dtype == MUIR_BF16 && a->T > 0 && (int64_t)a->H * a->dk >= 64 && (int64_t)a->H * a->dv >= 64;
 }
